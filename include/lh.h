@@ -66,7 +66,8 @@ typedef enum {
   LH_ERR_UNSUPPORTED = 2,  /* valid for the method, not built here (d, p, L, dtype) */
   LH_ERR_WORKSPACE = 3,    /* ctx or workspace smaller than the plan needs */
   LH_ERR_CUDA = 4,         /* a CUDA runtime call or launch failed */
-  LH_ERR_TIMEOUT = 5       /* a device-side wait gave up (see lh_device_status) */
+  LH_ERR_TIMEOUT = 5,      /* a device-side wait gave up (see lh_device_status) */
+  LH_ERR_PAGE = 6          /* a cache call met a row outside its pages (see lh_device_status) */
 } lh_status;
 
 typedef enum { LH_F32 = 0, LH_BF16 = 1 } lh_dtype;
@@ -262,9 +263,144 @@ lh_status lh_backward(const lh_plan* plan, const void* dO, const void* ctx, size
                       void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes,
                       lh_stream_t stream);
 
-/* Device-side status word: LH_OK, or LH_ERR_TIMEOUT if a bounded wait inside
- * a kernel gave up since the last reset.  Synchronises the current device;
- * reset != 0 clears the word. */
+/* --- Rotary positions ------------------------------------------------------
+ * Positions for the layer's Q and K: channel pairs of a row at position t are
+ * turned by the angle t * f_i,
+ *     (a, b) -> m * (a cos - b sin, b cos + a sin),
+ * i = 0 .. rot/2 - 1, and channels rot .. d-1 pass unchanged.  The unscaled
+ * frequencies are base^(-2 i / rot).  For contexts longer than the ones a
+ * model was trained on they are scaled:
+ *   LH_SCALE_LINEAR  f / factor;
+ *   LH_SCALE_BANDS   with r = original * f / (2 pi), the turns a pair makes in
+ *                    `original` positions, and g = (r - low) / (high - low)
+ *                    clamped to [0, 1]:  (1 - g) * f / factor + g * f.
+ * m (`magnitude`, 1 for none) multiplies every turned channel. */
+typedef enum {
+  LH_ROTARY_HALF = 0,        /* pairs (i, i + rot/2) */
+  LH_ROTARY_INTERLEAVED = 1  /* pairs (2 i, 2 i + 1) */
+} lh_rotary_layout;
+typedef enum { LH_SCALE_NONE = 0, LH_SCALE_LINEAR = 1, LH_SCALE_BANDS = 2 } lh_rotary_scaling;
+#define LH_MAX_PAIRS 64
+
+typedef struct {
+  int32_t d, rot, layout, scaling; /* head dimension, turned channels, lh_rotary_layout, lh_rotary_scaling */
+  double base, factor, low, high, original, magnitude;
+} lh_rotary_config;
+
+/* turns[i]: the fraction of a full turn that pair i makes per position, as a
+ * 64-bit fixed-point fraction (2^64 = one turn).  A position times it wraps to
+ * the angle modulo a turn exactly, so far positions lose nothing. */
+typedef struct {
+  lh_rotary_config c;
+  uint64_t turns[LH_MAX_PAIRS];
+} lh_rotary_plan;
+
+/* Fill *out from *cfg.  Host only.  LH_ERR_INVALID_ARG: rot not in 1..d,
+ * base or magnitude (or, where the scaling uses them, factor or original) not
+ * positive and finite, not 0 <= low < high with bands, an unknown layout or
+ * scaling.  LH_ERR_UNSUPPORTED: d not in {64, 128}, rot not a multiple of
+ * 16. */
+lh_status lh_rotary_init(const lh_rotary_config* cfg, lh_rotary_plan* out);
+int64_t lh_rotary_plan_bytes(void);
+
+/* A [B, H, N, d] tensor by its strides, in elements; the d channels of a row
+ * are contiguous and every row starts on a 16-byte boundary. */
+typedef struct {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_n;
+  int64_t H;
+} lh_rows;
+
+/* Turn `count` tensors (1 or 2: Q, or Q and K; their H may differ) of B
+ * sequences of N rows: Y[i] from X[i].  Row n of sequence b stands at
+ * positions[b * positions_stride + n], or at start + n where positions is
+ * NULL.  transpose != 0 applies the transposed map, which is the gradient of
+ * the plain one.  Y[i] may be X[i] itself (same pointer and strides);
+ * otherwise none of the Y may overlap another tensor of the call.  Inputs may
+ * repeat rows by zero strides, outputs may not.  fp32 arithmetic, rounded
+ * once. */
+lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_t N, int32_t count,
+                    const lh_rows* X, const lh_rows* Y, const int32_t* positions,
+                    int64_t positions_stride, int64_t start, int32_t transpose,
+                    lh_stream_t stream);
+
+/* --- Paged key-value cache ---------------------------------------------------
+ * The layer itself needs all queries at once; the trained model answers token
+ * by token with dense attention over a cache.  Keys and values live in pages
+ * of `page` rows, [pages, H, page, d] each (one head's rows of a page are
+ * contiguous).  Slot j of sequence b is row j % page of page
+ * table[b * table_stride + j / page]; the sequence holds slots 0 ..
+ * lengths[b] - 1, and its capacity is width * page slots.  table and lengths
+ * are read on the device when the call runs, so a captured graph follows
+ * their contents.  A length outside 0 .. capacity is clamped, a row whose
+ * page index is outside 0 .. pages - 1 is left out (not written, not
+ * attended to), and either sets the device status word to LH_ERR_PAGE.
+ * Built here: d in {64, 128}, page a power of two, 16 to 65536, capacity below
+ * 2^31 - 2^16.  Index arrays (table, lengths, counts, positions, protect) need
+ * 4-byte alignment only. */
+typedef struct {
+  void *k, *v;            /* [pages, H, page, d] */
+  int64_t pages;
+  int32_t H, page, d, dtype;
+  const int32_t* table;   /* [B, width] */
+  int64_t table_stride;   /* elements from one sequence's row to the next */
+  int32_t B, width;
+  const int32_t* lengths; /* [B] */
+} lh_cache;
+int64_t lh_cache_bytes(void); /* sizeof(lh_cache), for bindings */
+
+/* Write the newest rows of each sequence: row t of K and V ([B, H, T, d]),
+ * t < counts[b] (T where counts is NULL), goes to slot
+ * lengths[b] - counts[b] + t; lengths already count the new rows.  Rows from
+ * counts[b] on are padding and are not read.  With `rotary`, K (and Q) rows are
+ * turned at positions[b * positions_stride + t], or at their slot where
+ * positions is NULL; without it they are copied.  Q ([B, Hq, T, d], Q and Qo
+ * both or neither) goes to Qo, which may be Q itself; its padding rows become
+ * zero.  slot_positions ([B, H, capacity], or NULL) receives each new slot's
+ * position.  Rows of two sequences must not share a slot of a page. */
+lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, int64_t T,
+                          const lh_rows* K, const lh_rows* V, const lh_rows* Q, const lh_rows* Qo,
+                          const int32_t* positions, int64_t positions_stride,
+                          const int32_t* counts, int32_t* slot_positions, lh_stream_t stream);
+
+/* Attention of one new token of each sequence over its cache:
+ *   s_j = scale * q . k_j (j < lengths[b]),  lse = log sum_j exp s_j,
+ *   O = sum_j exp(s_j - lse) v_j;  an empty sequence gives O = 0, lse = -inf.
+ * Q: [B, Hq, 1, d] (stride_n is not used), Hq a multiple of the cache's H;
+ * query heads h * Hq/H .. share key head h.  O: [B, Hq, d] contiguous, lse:
+ * [B, Hq] fp32.  weights and weights_out ([B, H, capacity] fp32, both or
+ * neither, possibly the same array): for every slot j < lengths[b]
+ *   weights_out[b,h,j] = weights[b,h,j] + sum over head h's queries exp(s_j - lse);
+ * the entries behind are not touched.  ws: lh_decode_ws_bytes() bytes, contents
+ * on entry ignored; calls that overlap on the GPU (two streams, two graphs)
+ * need one each.  Results do not depend on scheduling. */
+int64_t lh_decode_ws_bytes(const lh_cache* cache, int64_t Hq, int32_t with_weights);
+lh_status lh_decode(const lh_cache* cache, const lh_rows* Q, float scale, void* O, float* lse,
+                    const float* weights, float* weights_out, void* ws, size_t ws_bytes,
+                    lh_stream_t stream);
+
+/* Keep the `budget` best rows of each (b, h) and give up the others.  With
+ * n = lengths[b] and m = min(n, budget), the m rows kept are the first by
+ * (protected, larger weight, lower slot); a row is protected when its position
+ * (positions[b,h,j], or j where positions is NULL) is at or above protect[b]
+ * (protect NULL: none is).  A NaN weight ranks below all others.  Kept rows in slots below m stay where they are;
+ * the i-th kept row at a slot from m on moves, key and value, to the i-th
+ * given-up slot below m (both in ascending order).  weights_out and
+ * positions_out ([B, H, capacity]; they may be weights and positions) follow the
+ * rows; behind slot m they become 0 and -1.  lengths_out ([B], not the cache's
+ * lengths) receives m.  positions and positions_out: both or neither.  Pages
+ * behind slot m hold nothing any more.  A row whose page is bad is left where
+ * it is (its weight still moves).  No two sequences may share a page.  ws as in lh_decode. */
+int64_t lh_evict_ws_bytes(const lh_cache* cache, int64_t budget);
+lh_status lh_evict(const lh_cache* cache, int64_t budget, const float* weights,
+                   const int32_t* positions, const int32_t* protect, float* weights_out,
+                   int32_t* positions_out, int32_t* lengths_out, void* ws, size_t ws_bytes,
+                   lh_stream_t stream);
+
+/* Device-side status word: LH_OK, LH_ERR_TIMEOUT if a bounded wait inside
+ * a kernel gave up since the last reset, or else LH_ERR_PAGE if a cache call
+ * met a page index, a length or a count outside the cache (it left those
+ * rows out).  Synchronises the current device; reset != 0 clears the word. */
 lh_status lh_device_status(int reset);
 
 /* Self-test of that failure path: enqueues one CTA that waits, through the

@@ -9,8 +9,9 @@
 
 namespace lh {
 
-// Device status word (LH_OK or LH_ERR_TIMEOUT); kernels with bounded waits
-// receive its address from device_status_ptr().
+// Device status word (LH_OK or LH_ERR_TIMEOUT, and the bit kStatusPage);
+// kernels with bounded waits and the cache kernels receive its address from
+// device_status_ptr().
 static __device__ unsigned int g_device_status = 0;
 
 unsigned int* device_status_ptr() {
@@ -88,6 +89,7 @@ const char* lh_status_string(lh_status s) {
     case LH_ERR_WORKSPACE: return "workspace too small";
     case LH_ERR_CUDA: return "CUDA error";
     case LH_ERR_TIMEOUT: return "device-side wait timed out";
+    case LH_ERR_PAGE: return "row outside the cache";
   }
   return "unknown status";
 }
@@ -200,17 +202,6 @@ static lh_status check_plan(const lh_plan* plan) {
     return fail(LH_ERR_INVALID_ARG, "plan does not match its config (not from lh_plan_init?)");
   return LH_OK;
 }
-
-#define LH_CHECK_PTR(ptr)                                                      \
-  do {                                                                         \
-    if (!aligned16(ptr)) return fail(LH_ERR_INVALID_ARG, #ptr " is null or not 16-byte aligned"); \
-  } while (0)
-
-#define LH_TRY(expr)                    \
-  do {                                  \
-    lh_status s_ = (expr);              \
-    if (s_ != LH_OK) return s_;         \
-  } while (0)
 
 lh_status lh_pyramid(const lh_plan* plan, const void* Q, const void* K, const void* V,
                      void* pyrQ, void* pyrK, void* pyrV, lh_stream_t stream) {
@@ -462,7 +453,8 @@ lh_status lh_device_status(int reset) {
     e = cudaMemcpyToSymbol(g_device_status, &z, sizeof(z));
     if (e != cudaSuccess) return cuda_status(e, "lh_device_status");
   }
-  if (v != 0) return fail(LH_ERR_TIMEOUT, "a bounded device-side wait gave up");
+  if (v & ~kStatusPage) return fail(LH_ERR_TIMEOUT, "a bounded device-side wait gave up");
+  if (v != 0) return fail(LH_ERR_PAGE, "a cache call met a page index, length or count outside the cache");
   return ok();
 }
 

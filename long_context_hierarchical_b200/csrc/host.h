@@ -31,12 +31,12 @@ Geo make_geo(const lh_plan& p);
 // Argument checks shared by the attention entry points (sizes, dtype, d).
 lh_status check_attn(int64_t BH, int64_t S, int32_t d, int32_t dtype);
 
-// Calls f.template operator()<T, D>() for the plan's storage type and head
-// dimension (d in {64, 128}, validated by lh_plan_init).
+// Calls f.template operator()<T, D>() for a storage type and head dimension
+// (d in {64, 128}, validated by the caller).
 template <typename F>
-void with_type_dim(const lh_plan& plan, F&& f) {
-  const bool bf = plan.c.dtype == LH_BF16;
-  if (plan.c.d == 128) {
+void with_type_dim(int dtype, int d, F&& f) {
+  const bool bf = dtype == LH_BF16;
+  if (d == 128) {
     if (bf) f.template operator()<__nv_bfloat16, 128>();
     else f.template operator()<float, 128>();
   } else {
@@ -44,7 +44,13 @@ void with_type_dim(const lh_plan& plan, F&& f) {
     else f.template operator()<float, 64>();
   }
 }
-// Device address of the status word that bounded waits set on timeout.
+template <typename F>
+void with_type_dim(const lh_plan& plan, F&& f) {
+  with_type_dim(plan.c.dtype, plan.c.d, static_cast<F&&>(f));
+}
+// Device address of the status word that bounded waits set on timeout and the
+// cache kernels (bit kStatusPage) on a row outside the cache.
+constexpr unsigned int kStatusPage = 8u;
 unsigned int* device_status_ptr();
 bool aligned16(const void* ptr);
 inline cudaStream_t as_cuda(lh_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
@@ -81,4 +87,37 @@ cudaError_t launch_attn_fwd_tc128(int64_t BH, int64_t S, const void* Q, const vo
 // One CTA waiting on a barrier nothing signals (the failure-path self-test).
 cudaError_t launch_wait_timeout_selftest(cudaStream_t st);
 
+// Rotary positions and the paged cache (sizes validated by the entry points).
+struct RowsArg {  // lh_rows as a kernel argument
+  void* ptr;
+  int64_t sb, sh, sn;
+  int H;
+};
+cudaError_t launch_rotary(const lh_rotary_plan& plan, int dtype, int64_t B, int64_t N, int count,
+                          const RowsArg* X, const RowsArg* Y, const int32_t* positions,
+                          int64_t positions_stride, int64_t start, bool transpose, cudaStream_t st);
+cudaError_t launch_cache_append(const lh_cache& c, const lh_rotary_plan* rotary, int64_t T,
+                                const RowsArg& K, const RowsArg& V, const RowsArg& Q, const RowsArg& Qo,
+                                const int32_t* positions, int64_t positions_stride,
+                                const int32_t* counts, int32_t* slot_positions, cudaStream_t st);
+int64_t decode_ws_bytes(const lh_cache& c, int64_t Hq, bool with_weights);
+cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void* O, float* lse,
+                          const float* weights, float* weights_out, void* ws, cudaStream_t st);
+int64_t evict_ws_bytes(const lh_cache& c, int64_t budget);
+cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights,
+                         const int32_t* positions, const int32_t* protect, float* weights_out,
+                         int32_t* positions_out, int32_t* lengths_out, void* ws, cudaStream_t st);
+
 }  // namespace lh
+
+#define LH_CHECK_PTR(ptr)                                                      \
+  do {                                                                         \
+    if (!aligned16(ptr)) return fail(LH_ERR_INVALID_ARG, #ptr " is null or not 16-byte aligned"); \
+  } while (0)
+
+#define LH_TRY(expr)                    \
+  do {                                  \
+    lh_status s_ = (expr);              \
+    if (s_ != LH_OK) return s_;         \
+  } while (0)
+

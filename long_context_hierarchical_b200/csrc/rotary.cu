@@ -1,0 +1,220 @@
+// Rotary positions on [B, H, N, d] tensors and the append of new rows to the
+// paged cache.
+//
+// (a, b) -> m (a cos - b sin, b cos + a sin) for every channel pair, the angle
+// being position * frequency; the transposed map (the gradient) turns the
+// other way.  Bound by HBM: every row is read and written once, about six
+// flops a pair.  The sines and cosines are formed in the kernel, once for a
+// (position, eight pairs) and all heads of Q and K: a table of them would be
+// read again for each call and cost a rounding of its own.
+#include <algorithm>
+
+#include "host.h"
+#include "rotary.cuh"
+
+namespace lh {
+namespace {
+
+constexpr int kRotThreads = 256;
+constexpr int kHeadsInFlight = 4;
+
+struct RotaryCall {
+  RowsArg x[2], y[2];
+  const int32_t* positions;
+  int64_t positions_stride, start;
+  int64_t N, rows;  // rows = B * N
+  int heads, group; // heads of both tensors, heads of one block
+  bool transpose;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRotThreads)
+rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ RotaryCall k) {
+  constexpr int U = D / 16;
+  const int64_t row = (int64_t)blockIdx.x * (kRotThreads / U) + threadIdx.x / U;
+  const int u = threadIdx.x % U;
+  if (row >= k.rows) return;
+  const int64_t b = row / k.N, n = row - b * k.N;
+  const Unit unit = make_unit(r, u);
+  float c[8], s[8];
+  if (unit.turn) {
+    const int64_t pos = k.positions ? (int64_t)k.positions[b * k.positions_stride + n] : k.start + n;
+    unit_angles(r, u, pos, k.transpose, c, s);
+  }
+  const int h0 = blockIdx.y * k.group;
+  const int h1 = min(k.heads, h0 + k.group);
+  for (int h = h0; h < h1; h += kHeadsInFlight) {
+    Chunk<T> a[kHeadsInFlight], e[kHeadsInFlight];
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      if (h + i >= h1) continue;
+      const int t = h + i >= k.x[0].H;
+      const RowsArg& x = k.x[t];
+      const T* p = static_cast<const T*>(x.ptr) + b * x.sb + (h + i - (t ? k.x[0].H : 0)) * x.sh + n * x.sn;
+      a[i].load(p + unit.ca * 8);
+      e[i].load(p + unit.cb * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      if (h + i >= h1) continue;
+      const int t = h + i >= k.x[0].H;
+      const RowsArg& y = k.y[t];
+      T* p = static_cast<T*>(y.ptr) + b * y.sb + (h + i - (t ? k.x[0].H : 0)) * y.sh + n * y.sn;
+      if (unit.turn) {
+        float xa[8], xb[8];
+        a[i].get(xa);
+        e[i].get(xb);
+        turn_unit(r.half, c, s, xa, xb);
+        Vec8<T>::store(p + unit.ca * 8, xa);
+        Vec8<T>::store(p + unit.cb * 8, xb);
+      } else {
+        a[i].store(p + unit.ca * 8);
+        e[i].store(p + unit.cb * 8);
+      }
+    }
+  }
+}
+
+struct AppendCall {
+  lh_cache c;
+  RowsArg q, qo, k, v;
+  const int32_t *positions, *counts;
+  int64_t positions_stride;
+  int32_t* slot_positions;
+  int64_t T, rows;  // rows = B * T
+  int group;        // heads of one block
+  int page_shift;
+  unsigned int* status;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kRotThreads)
+append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ AppendCall k) {
+  constexpr int U = D / 16;
+  const int64_t row = (int64_t)blockIdx.x * (kRotThreads / U) + threadIdx.x / U;
+  const int u = threadIdx.x % U;
+  if (row >= k.rows) return;
+  const int64_t b = row / k.T, t = row - b * k.T;
+  const int64_t count = k.counts ? (int64_t)k.counts[b] : k.T;
+  const int64_t capacity = (int64_t)k.c.width << k.page_shift;
+  const bool there = t < count;
+  const int64_t slot = (int64_t)k.c.lengths[b] - count + t;
+  // A row outside the cache is left out, and so is one of a batch whose count
+  // is more than the T rows that were given.
+  int64_t page = -1;
+  if (there && slot >= 0 && slot < capacity && count <= k.T) {
+    page = k.c.table[b * k.c.table_stride + (slot >> k.page_shift)];
+    if (page >= k.c.pages) page = -1;
+  }
+  const bool bad = there && page < 0;
+  if (u == 0 && blockIdx.y == 0 && (bad || (t == 0 && count < 0))) atomicOr(k.status, kStatusPage);
+  const int64_t pos = k.positions && there ? (int64_t)k.positions[b * k.positions_stride + t] : slot;
+  const Unit unit = make_unit(r, u);
+  float c[8], s[8];
+  if (unit.turn) unit_angles(r, u, pos, false, c, s);
+
+  const int Hq = k.q.H, H = k.c.H;
+  const int h0 = blockIdx.y * k.group;
+  const int h1 = min(Hq + 2 * H, h0 + k.group);
+  const int64_t in_page = slot & ((1 << k.page_shift) - 1);
+  for (int h = h0; h < h1; ++h) {
+    Chunk<T> a, e;
+    const bool is_q = h < Hq, is_k = !is_q && h < Hq + H;
+    const int head = is_q ? h : is_k ? h - Hq : h - Hq - H;
+    const RowsArg& x = is_q ? k.q : is_k ? k.k : k.v;
+    T* out;
+    if (is_q) {
+      out = static_cast<T*>(k.qo.ptr) + b * k.qo.sb + head * k.qo.sh + t * k.qo.sn;
+      if (!there) {
+        a.zero();
+        a.store(out + unit.ca * 8);
+        a.store(out + unit.cb * 8);
+        continue;
+      }
+    } else {
+      if (page < 0) continue;
+      out = static_cast<T*>(is_k ? k.c.k : k.c.v) + (((page * H + head) << k.page_shift) + in_page) * D;
+      if (is_k && u == 0 && k.slot_positions)
+        k.slot_positions[(b * H + head) * capacity + slot] = (int32_t)pos;
+    }
+    const T* p = static_cast<const T*>(x.ptr) + b * x.sb + head * x.sh + t * x.sn;
+    a.load(p + unit.ca * 8);
+    e.load(p + unit.cb * 8);
+    if (unit.turn && (is_q || is_k)) {
+      float xa[8], xb[8];
+      a.get(xa);
+      e.get(xb);
+      turn_unit(r.half, c, s, xa, xb);
+      Vec8<T>::store(out + unit.ca * 8, xa);
+      Vec8<T>::store(out + unit.cb * 8, xb);
+    } else {
+      a.store(out + unit.ca * 8);
+      e.store(out + unit.cb * 8);
+    }
+  }
+}
+
+// Heads that one block takes: all of them where the rows alone fill the GPU
+// (the sines and cosines are then formed once), fewer for few rows.
+int head_group(int64_t blocks, int heads) {
+  int g = heads;
+  while (g > 1 && blocks * ((heads + g - 1) / g) < 148 * 8) g = (g + 1) / 2;
+  return g;
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const lh_rotary_plan& plan, int dtype, int64_t B, int64_t N, int count,
+                          const RowsArg* X, const RowsArg* Y, const int32_t* positions,
+                          int64_t positions_stride, int64_t start, bool transpose, cudaStream_t st) {
+  RotaryCall k{};
+  for (int i = 0; i < count; ++i) {
+    k.x[i] = X[i];
+    k.y[i] = Y[i];
+  }
+  k.positions = positions;
+  k.positions_stride = positions_stride;
+  k.start = start;
+  k.N = N;
+  k.rows = B * N;
+  k.heads = k.x[0].H + k.x[1].H;
+  k.transpose = transpose;
+  const int64_t per = kRotThreads / (plan.c.d / 16);
+  const int64_t blocks = (k.rows + per - 1) / per;
+  k.group = head_group(blocks, k.heads);
+  const dim3 grid((unsigned)blocks, (k.heads + k.group - 1) / k.group);
+  const RotaryArg r = make_rotary_arg(&plan);
+  with_type_dim(dtype, plan.c.d, [&]<typename T, int D>() { rotary_kernel<T, D><<<grid, kRotThreads, 0, st>>>(r, k); });
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cache_append(const lh_cache& c, const lh_rotary_plan* rotary, int64_t T,
+                                const RowsArg& K, const RowsArg& V, const RowsArg& Q, const RowsArg& Qo,
+                                const int32_t* positions, int64_t positions_stride,
+                                const int32_t* counts, int32_t* slot_positions, cudaStream_t st) {
+  AppendCall k{};
+  k.c = c;
+  k.q = Q;
+  k.qo = Qo;
+  k.k = K;
+  k.v = V;
+  k.positions = positions;
+  k.positions_stride = positions_stride;
+  k.counts = counts;
+  k.slot_positions = slot_positions;
+  k.T = T;
+  k.rows = (int64_t)c.B * T;
+  k.page_shift = __builtin_ctz(c.page);
+  k.status = device_status_ptr();
+  if (!k.status) return cudaErrorInvalidSymbol;
+  const int64_t per = kRotThreads / (c.d / 16);
+  const int64_t blocks = (k.rows + per - 1) / per;
+  const int heads = Q.H + 2 * c.H;
+  k.group = head_group(blocks, heads);
+  const dim3 grid((unsigned)blocks, (heads + k.group - 1) / k.group);
+  const RotaryArg r = make_rotary_arg(rotary);
+  with_type_dim(c.dtype, c.d, [&]<typename E, int D>() { append_kernel<E, D><<<grid, kRotThreads, 0, st>>>(r, k); });
+  return cudaGetLastError();
+}
+
+}  // namespace lh

@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # compiled with different tile constants); the default is the in-tree one.
 LIB_PATH = os.environ.get("LH_LIBRARY") or os.path.join(HERE, "liblh.so")
 
-LH_OK, LH_ERR_INVALID_ARG, LH_ERR_UNSUPPORTED, LH_ERR_WORKSPACE, LH_ERR_CUDA, LH_ERR_TIMEOUT = range(6)
+(LH_OK, LH_ERR_INVALID_ARG, LH_ERR_UNSUPPORTED, LH_ERR_WORKSPACE, LH_ERR_CUDA, LH_ERR_TIMEOUT,
+ LH_ERR_PAGE) = range(7)
 LH_F32, LH_BF16 = 0, 1
 MAX_LEVELS = 8
 DTYPES = {"f32": LH_F32, "bf16": LH_BF16}
@@ -29,7 +30,9 @@ EXPORTS = (
     "lh_attn_fwd", "lh_attn_bwd_ws_bytes", "lh_attn_bwd", "lh_scatter", "lh_scatter_bwd",
     "lh_gather_bwd", "lh_forward", "lh_backward", "lh_device_status", "lh_status_string",
     "lh_last_error", "lh_plan_bytes", "lh_attn_bwd_static", "lh_set_deterministic",
-    "lh_selftest_wait_timeout",
+    "lh_selftest_wait_timeout", "lh_rotary_init", "lh_rotary_plan_bytes", "lh_rotary",
+    "lh_cache_bytes", "lh_cache_append", "lh_decode_ws_bytes", "lh_decode", "lh_evict_ws_bytes",
+    "lh_evict",
 )
 
 
@@ -56,6 +59,32 @@ class LhPlan(ctypes.Structure):
         "ctx_sel_idx", "ctx_slot_of", "ctx_Qg", "ctx_Kg", "ctx_Vg", "ctx_Og", "ctx_lse",
         "ws_pyrQ", "ws_pyrK", "ws_pyrV", "ws_scores", "ws_topk",
         "ws_dOg", "ws_D", "ws_dQg", "ws_dKg", "ws_dVg", "ws_attn")]
+
+
+MAX_PAIRS = 64
+LAYOUT = {"half": 0, "interleaved": 1}
+SCALING = {"none": 0, "linear": 1, "bands": 2}
+_I32, _F64 = ctypes.c_int32, ctypes.c_double
+
+
+class LhRotaryConfig(ctypes.Structure):
+    _fields_ = [(n, _I32) for n in ("d", "rot", "layout", "scaling")] + \
+        [(n, _F64) for n in ("base", "factor", "low", "high", "original", "magnitude")]
+
+
+class LhRotaryPlan(ctypes.Structure):
+    _fields_ = [("c", LhRotaryConfig), ("turns", ctypes.c_uint64 * MAX_PAIRS)]
+
+
+class LhRows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", _I64), ("stride_h", _I64), ("stride_n", _I64),
+                ("H", _I64)]
+
+
+class LhCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", _I64), ("H", _I32),
+                ("page", _I32), ("d", _I32), ("dtype", _I32), ("table", ctypes.c_void_p),
+                ("table_stride", _I64), ("B", _I32), ("width", _I32), ("lengths", ctypes.c_void_p)]
 
 
 class LighthouseError(RuntimeError):
@@ -89,6 +118,11 @@ def _load():
         "lh_device_status": (ctypes.c_int,),
         "lh_selftest_wait_timeout": (P,),
         "lh_attn_bwd_static": (I64, I64, I32, I32, P, P, P, P, P, P, P, P, P, P),
+        "lh_rotary_init": (ctypes.POINTER(LhRotaryConfig), ctypes.POINTER(LhRotaryPlan)),
+        "lh_rotary": (ctypes.POINTER(LhRotaryPlan), I32, I64, I64, I32, P, P, P, I64, I64, I32, P),
+        "lh_cache_append": (ctypes.POINTER(LhCache), P, I64, P, P, P, P, P, I64, P, P, P),
+        "lh_decode": (ctypes.POINTER(LhCache), P, ctypes.c_float, P, P, P, P, P, SZ, P),
+        "lh_evict": (ctypes.POINTER(LhCache), I64, P, P, P, P, P, P, P, SZ, P),
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -104,8 +138,15 @@ def _load():
     lib.lh_plan_bytes.restype = I64
     lib.lh_set_deterministic.argtypes = [ctypes.c_int]
     lib.lh_set_deterministic.restype = None
+    lib.lh_decode_ws_bytes.argtypes = [ctypes.POINTER(LhCache), I64, I32]
+    lib.lh_evict_ws_bytes.argtypes = [ctypes.POINTER(LhCache), I64]
+    for name in ("lh_decode_ws_bytes", "lh_evict_ws_bytes", "lh_rotary_plan_bytes", "lh_cache_bytes"):
+        getattr(lib, name).restype = I64
     if lib.lh_plan_bytes() != ctypes.sizeof(LhPlan):
         raise ImportError("lh_plan layout of liblh.so does not match this binding")
+    if lib.lh_rotary_plan_bytes() != ctypes.sizeof(LhRotaryPlan) or \
+            lib.lh_cache_bytes() != ctypes.sizeof(LhCache):
+        raise ImportError("lh_rotary_plan or lh_cache layout of liblh.so does not match this binding")
     return lib
 
 
@@ -358,6 +399,394 @@ def gather_bwd(pl: Plan, dQg, dKg, dVg, slot_of, stream=None):
     return out
 
 
+# --- rotary positions ---------------------------------------------------------
+
+
+def _run(dev, stream, inputs, call):
+    """``call(handle)`` enqueues on ``stream`` (default: the device's current one)
+    and returns the tensors it allocated, with ``dev`` as the current device.
+
+    On a stream other than the current one the outputs come from that stream's
+    memory pool, and every tensor is recorded on the stream it is used on next
+    to its own, so that none is handed out again while the other one works."""
+    cur = torch.cuda.current_stream(dev)
+    if stream is None or stream == cur:
+        if dev.index == torch.cuda.current_device():
+            return call(ctypes.c_void_p(cur.cuda_stream))
+        with torch.cuda.device(dev):
+            return call(ctypes.c_void_p(cur.cuda_stream))
+    if stream.device != dev:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
+    with torch.cuda.stream(stream):
+        outs = call(ctypes.c_void_p(stream.cuda_stream))
+    for t in inputs:
+        if t is not None:
+            t.record_stream(stream)
+    for t in outs:
+        if t is not None:
+            t.record_stream(cur)
+    return outs
+
+
+def _on_device(dev, **tensors):
+    if dev.type != "cuda":
+        raise ValueError(f"{next(iter(tensors))}: must be a CUDA tensor (got {dev})")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+
+
+def _strided(t, name: str, dtype, shape):
+    """Check a [B, H, N, d] tensor that the library reads or writes by its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 4 or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        want = ", ".join("*" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{want}]")
+    if t.stride(3) != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+
+
+def _lh_rows(t):
+    s = t.stride()
+    return LhRows(t.data_ptr(), s[0], s[1], s[2], t.shape[1])
+
+
+def _index(t, name: str, shape):
+    """Check an int32 index tensor; returns it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t
+
+
+def _positions(t, B: int, N: int):
+    """Row stride of a positions tensor of shape [N], [1, N] or [B, N]."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"positions: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != torch.int32:
+        raise ValueError(f"positions: dtype {t.dtype}, expected torch.int32")
+    if tuple(t.shape) not in ((N,), (1, N), (B, N)):
+        raise ValueError(f"positions: shape {tuple(t.shape)}, expected [{N}] or [{B}, {N}]")
+    if N > 1 and t.stride(-1) != 1:
+        raise ValueError("positions: a sequence's positions must be contiguous")
+    return t.stride(0) if t.dim() == 2 and t.shape[0] > 1 else 0
+
+
+@dataclass
+class RotaryPlan:
+    """Frequencies and pair layout of a rotation (from lh_rotary_init)."""
+    raw: LhRotaryPlan
+
+    @property
+    def d(self):
+        return self.raw.c.d
+
+
+def rotary_plan(d: int = 64, rot: int | None = None, base: float = 10000.0, layout: str = "half",
+                scaling: str = "none", factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                original: float = 0.0, magnitude: float = 1.0) -> RotaryPlan:
+    """rot: turned channels (default all d); layout: "half" pairs channels
+    (i, i + rot/2), "interleaved" (2i, 2i + 1); scaling: "none", "linear"
+    (every frequency divided by factor) or "bands" (slow pairs divided, fast
+    ones kept: those that make more than ``high`` turns in ``original``
+    positions, with a ramp down to ``low``); magnitude multiplies every turned channel."""
+    cfg = LhRotaryConfig(d, d if rot is None else rot, LAYOUT[layout], SCALING[scaling], base, factor,
+                         low, high, original, magnitude)
+    raw = LhRotaryPlan()
+    _check(LIB.lh_rotary_init(ctypes.byref(cfg), ctypes.byref(raw)), "lh_rotary_init")
+    return RotaryPlan(raw)
+
+
+def _rotate(rp: RotaryPlan, X, Y, positions, start, transpose, stream):
+    """Turn the one or two tensors X into Y (None: new contiguous tensors)."""
+    first = X[0]
+    if not isinstance(first, torch.Tensor) or first.dim() != 4:
+        raise ValueError("Q: expected a tensor of shape [B, H, N, d]")
+    if first.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"Q: dtype {first.dtype}, expected torch.bfloat16 or torch.float32")
+    B, _, N, _ = first.shape
+    named = dict(zip(("Q", "K"), X))
+    for name, t in named.items():
+        _strided(t, name, first.dtype, (B, None, N, rp.d))
+    if Y is not None:
+        for x, (name, t) in zip(X, zip(("out[0]", "out[1]"), Y)):
+            _strided(t, name, first.dtype, x.shape)
+            named[name] = t
+    stride = _positions(positions, B, N)
+    dev = first.device
+    _on_device(dev, **named, positions=positions)
+
+    def call(handle):
+        out = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in X) if Y is None else Y
+        n = len(X)
+        xs, ys = (LhRows * n)(*map(_lh_rows, X)), (LhRows * n)(*map(_lh_rows, out))
+        if first.numel() or X[-1].numel():
+            _check(LIB.lh_rotary(ctypes.byref(rp.raw), _dtype_code(first), B, N, n, xs, ys, _ptr(positions),
+                                 stride, start, transpose, handle), "lh_rotary")
+        return out
+
+    return _run(dev, stream, (*X, positions), call)
+
+
+def _pair(Q, K, out):
+    if K is None:
+        return (Q,), None if out is None else (out,)
+    if out is not None and len(out) != 2:
+        raise ValueError("out: expected two tensors")
+    return (Q, K), None if out is None else tuple(out)
+
+
+def rotary(rp: RotaryPlan, Q, K=None, positions=None, start: int = 0, out=None, stream=None):
+    """Q, or (Q, K), [B, H, N, d] with any strides between rows, turned to their
+    positions: positions[b, n] (int32, [N] or [B, N]) or start + n.  Returns new
+    contiguous tensors, or writes ``out`` (which may be the inputs themselves)."""
+    X, Y = _pair(Q, K, out)
+    got = _rotate(rp, X, Y, positions, start, 0, stream)
+    return got[0] if K is None else got
+
+
+def rotary_bwd(rp: RotaryPlan, dQ, dK=None, positions=None, start: int = 0, out=None, stream=None):
+    """Gradients of ``rotary``'s inputs from those of its outputs: the transposed map."""
+    X, Y = _pair(dQ, dK, out)
+    got = _rotate(rp, X, Y, positions, start, 1, stream)
+    return got[0] if dK is None else got
+
+
+# --- paged key-value cache ------------------------------------------------------
+
+
+class PagedCache:
+    """Keys and values of many sequences in pages: ``k`` and ``v``, [pages, H, page, d].
+
+    A sequence is a row of a page table ([B, width] int32) and a length
+    ([B] int32), both on the device and kept by the caller; slot j of sequence
+    b is row j % page of page table[b, j // page].  Rows behind a length are
+    never read."""
+
+    def __init__(self, pages: int, page: int, H: int, d: int = 64, dtype: str = "bf16", device="cuda"):
+        shape = (pages, H, page, d)
+        self._set(*(torch.empty(shape, dtype=TORCH_DTYPE[DTYPES[dtype]], device=device) for _ in range(2)))
+
+    @classmethod
+    def of(cls, k, v):
+        """A cache over existing tensors."""
+        self = cls.__new__(cls)
+        self._set(k, v)
+        return self
+
+    def _set(self, k, v):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: expected a tensor of shape [pages, H, page, d]")
+        if k.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"k: dtype {k.dtype}, expected torch.bfloat16 or torch.float32")
+        _strided(v, "v", k.dtype, k.shape)
+        for name, t in (("k", k), ("v", v)):
+            if not t.is_contiguous():
+                raise ValueError(f"{name}: must be contiguous")
+        if v.device != k.device:
+            raise ValueError(f"v: on {v.device}, k on {k.device}")
+        self.k, self.v = k, v
+        self.pages, self.H, self.page, self.d = k.shape
+
+    @property
+    def dtype(self):
+        return self.k.dtype
+
+    def _raw(self, table, lengths):
+        """The C view of the cache with one batch's table and lengths."""
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table: expected a tensor of shape [B, width]")
+        if table.dtype != torch.int32:
+            raise ValueError(f"table: dtype {table.dtype}, expected torch.int32")
+        B, width = table.shape
+        if width > 1 and table.stride(1) != 1:
+            raise ValueError("table: a sequence's pages must be contiguous")
+        _index(lengths, "lengths", (B,))
+        return LhCache(self.k.data_ptr(), self.v.data_ptr(), self.pages, self.H, self.page, self.d,
+                       _dtype_code(self.k), table.data_ptr(), table.stride(0), B, width,
+                       lengths.data_ptr()), B, width * self.page
+
+
+def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: RotaryPlan | None = None,
+                 positions=None, counts=None, slot_positions=None, out=None, stream=None):
+    """Write the new rows K, V ([B, H, T, d], any strides between rows) into the cache.
+
+    ``lengths`` already count the new rows: row t < counts[b] (default T) goes
+    to slot lengths[b] - counts[b] + t, rows behind are padding.  With
+    ``rotary`` the keys, and the queries Q ([B, Hq, T, d]), are turned at
+    positions ([T] or [B, T] int32, default: the slot).  Returns the turned
+    queries (padding rows zero), in ``out`` if given (which may be Q), or None.  ``slot_positions`` ([B, H,
+    capacity] int32) receives the positions of the new slots."""
+    if not isinstance(K, torch.Tensor) or K.dim() != 4:
+        raise ValueError("K: expected a tensor of shape [B, H, T, d]")
+    raw, B, capacity = cache._raw(table, lengths)
+    T = K.shape[2]
+    shape = (B, cache.H, T, cache.d)
+    named = {"K": K, "V": V, "table": table, "lengths": lengths, "positions": positions,
+             "counts": counts, "slot_positions": slot_positions, "Q": Q, "out": out}
+    for name in ("K", "V"):
+        _strided(named[name], name, cache.dtype, shape)
+    if Q is not None:
+        _strided(Q, "Q", cache.dtype, (B, None, T, cache.d))
+        if out is not None:
+            _strided(out, "out", cache.dtype, Q.shape)
+    elif out is not None:
+        raise ValueError("out: given without Q")
+    stride = _positions(positions, B, T)
+    if counts is not None:
+        _index(counts, "counts", (B,))
+    if slot_positions is not None:
+        _index(slot_positions, "slot_positions", (B, cache.H, capacity))
+    if rotary is not None and rotary.d != cache.d:
+        raise ValueError(f"rotary: for d = {rotary.d}, the cache has d = {cache.d}")
+    dev = cache.k.device
+    _on_device(dev, cache=cache.k, **named)
+
+    def call(handle):
+        qo = out
+        if Q is not None and out is None:
+            qo = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        if T and B:
+            rows = [None if t is None else ctypes.byref(_lh_rows(t)) for t in (K, V, Q, qo)]
+            _check(LIB.lh_cache_append(ctypes.byref(raw), None if rotary is None else ctypes.byref(rotary.raw),
+                                       T, *rows, _ptr(positions), stride, _ptr(counts), _ptr(slot_positions),
+                                       handle), "lh_cache_append")
+        return (qo,)
+
+    return _run(dev, stream, (*named.values(), cache.k, cache.v), call)[0]
+
+
+def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, weights=None,
+           weights_out=None, ws=None, stream=None):
+    """Attention of one new token of each sequence, Q [B, Hq, 1, d], over its
+    cache: (O [B, Hq, 1, d], lse [B, Hq, 1]).  Hq is a multiple of the cache's
+    H; neighbouring query heads share a key head.  An empty sequence gives
+    O = 0 and lse = -inf.  scale: default 1 / sqrt(d).  ``weights`` ([B, H,
+    capacity] fp32): each slot's attention probability, summed over the query
+    heads of its key head, is added to it, in place or into ``weights_out``.
+    ws: a uint8 scratch tensor of decode_ws_bytes(); calls that overlap on the
+    GPU need one each (default: a new one)."""
+    raw, B, capacity = cache._raw(table, lengths)
+    _strided(Q, "Q", cache.dtype, (B, None, 1, cache.d))
+    Hq = Q.shape[1]
+    if weights is None and weights_out is not None:
+        raise ValueError("weights_out: given without weights")
+    if weights is not None:
+        if weights_out is None:
+            weights_out = weights
+        for name, t in (("weights", weights), ("weights_out", weights_out)):
+            _slots(t, name, torch.float32, (B, cache.H, capacity))
+    dev = cache.k.device
+    need = _ws_need(LIB.lh_decode_ws_bytes(ctypes.byref(raw), Hq, 0 if weights is None else 1),
+                    "lh_decode_ws_bytes", B)
+    if ws is not None:
+        _require(ws, "ws", torch.uint8, need)
+    _on_device(dev, cache=cache.k, table=table, lengths=lengths, Q=Q, weights=weights,
+               weights_out=weights_out, ws=ws)
+
+    def call(handle):
+        o = torch.empty((B, Hq, 1, cache.d), dtype=Q.dtype, device=dev)
+        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=dev)
+        w = _bytes(need, dev) if ws is None else ws
+        if B:
+            q = _lh_rows(Q)
+            _check(LIB.lh_decode(ctypes.byref(raw), ctypes.byref(q),
+                                 cache.d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(weights),
+                                 _ptr(weights_out), _ptr(w), w.numel(), handle), "lh_decode")
+        return o, lse
+
+    return _run(dev, stream, (cache.k, cache.v, table, lengths, Q, weights, weights_out, ws), call)
+
+
+def _slots(t, name: str, dtype, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _ws_need(n: int, where: str, B: int) -> int:
+    if n < 0 and B:
+        _check(LH_ERR_INVALID_ARG, where)
+    return max(n, 0)
+
+
+def decode_ws_bytes(cache: PagedCache, table, lengths, Hq: int, with_weights: bool = False) -> int:
+    """Bytes of scratch that ``decode`` needs for this batch."""
+    raw, B, _ = cache._raw(table, lengths)
+    return _ws_need(LIB.lh_decode_ws_bytes(ctypes.byref(raw), Hq, int(with_weights)), "lh_decode_ws_bytes", B)
+
+
+def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=None, protect=None,
+          weights_out=None, positions_out=None, ws=None, stream=None):
+    """Keep the ``budget`` rows of largest weight of every sequence and head
+    (ties: the lower slot) and give up the others, moving keys and values
+    within their pages; returns (lengths, weights, positions) of what is left.
+
+    weights: [B, H, capacity] fp32, as ``decode`` sums them.  Rows at or above
+    position protect[b] ([B] int32) are kept before all others; positions
+    ([B, H, capacity] int32, default: the slot) say where rows stand once
+    earlier evictions have moved them.  Kept rows at low slots stay, the others
+    fill the slots given up, so the order of slots is not that of positions;
+    behind the new length weights are 0 and positions -1.  weights_out and
+    positions_out (default: new tensors) may be the inputs themselves.  ws: a
+    uint8 scratch tensor of evict_ws_bytes(); calls that overlap on the GPU
+    need one each (default: a new one)."""
+    raw, B, capacity = cache._raw(table, lengths)
+    shape = (B, cache.H, capacity)
+    _slots(weights, "weights", torch.float32, shape)
+    if weights_out is not None:
+        _slots(weights_out, "weights_out", torch.float32, shape)
+    if positions is None and positions_out is not None:
+        raise ValueError("positions_out: given without positions")
+    for name, t in (("positions", positions), ("positions_out", positions_out)):
+        if t is not None:
+            _slots(t, name, torch.int32, shape)
+    if protect is not None:
+        _index(protect, "protect", (B,))
+    dev = cache.k.device
+    need = _ws_need(LIB.lh_evict_ws_bytes(ctypes.byref(raw), budget), "lh_evict_ws_bytes", B)
+    if ws is not None:
+        _require(ws, "ws", torch.uint8, need)
+    _on_device(dev, cache=cache.k, table=table, lengths=lengths, weights=weights, weights_out=weights_out,
+               positions=positions, positions_out=positions_out, protect=protect, ws=ws)
+
+    def call(handle):
+        n = torch.empty((B,), dtype=torch.int32, device=dev)
+        wo = torch.empty(shape, dtype=torch.float32, device=dev) if weights_out is None else weights_out
+        po = positions_out
+        if positions is not None and po is None:
+            po = torch.empty(shape, dtype=torch.int32, device=dev)
+        w = _bytes(need, dev) if ws is None else ws
+        if B:
+            _check(LIB.lh_evict(ctypes.byref(raw), budget, _ptr(weights), _ptr(positions), _ptr(protect),
+                                _ptr(wo), _ptr(po), _ptr(n), _ptr(w), w.numel(), handle), "lh_evict")
+        return n, wo, po
+
+    return _run(dev, stream, (cache.k, cache.v, table, lengths, weights, weights_out, positions, positions_out,
+                              protect, ws), call)
+
+
+def evict_ws_bytes(cache: PagedCache, table, lengths, budget: int) -> int:
+    """Bytes of scratch that ``evict`` needs for this batch."""
+    raw, B, _ = cache._raw(table, lengths)
+    return _ws_need(LIB.lh_evict_ws_bytes(ctypes.byref(raw), budget), "lh_evict_ws_bytes", B)
+
+
 # --- whole layer --------------------------------------------------------------
 
 
@@ -367,6 +796,7 @@ class Context:
     def __init__(self, pl: Plan, device):
         self.plan = pl
         self.buf = _bytes(pl.raw.ctx_bytes, device)
+        self.rotary = None  # (plan, positions, start) of the forward's Q and K
 
     def _view(self, off, shape, dtype):
         n = 1
@@ -401,11 +831,22 @@ class Workspace:
         self.buf = _bytes(pl.raw.ws_bytes, device)
 
 
+def _bhnd(pl: Plan, *tensors):
+    """[B, H, N, d] views of contiguous tensors of at least that many elements."""
+    c = pl.raw.c
+    return tuple(t.view(-1)[: c.B * c.H * c.N * c.d].view(c.B, c.H, c.N, c.d) for t in tensors)
+
+
 def forward(pl: Plan, Q, K, V, O=None, ctx: Context | None = None, ws: Workspace | None = None,
-            stream=None):
-    """O = Lighthouse(Q, K, V); returns (O, ctx)."""
+            stream=None, rotary: RotaryPlan | None = None, positions=None, start: int = 0):
+    """O = Lighthouse(Q, K, V); returns (O, ctx).  With ``rotary`` the layer
+    runs on Q and K turned to their positions (copies, as ``lh.rotary`` makes
+    them), and the matching ``backward`` turns their gradients back; positions
+    must not change in between."""
     _require_tokens(pl, Q=Q, K=K, V=V)
     dev = Q.device
+    if rotary is not None:
+        Q, K = _rotate(rotary, _bhnd(pl, Q, K), None, positions, start, 0, stream)
     if O is None:
         O = torch.empty_like(Q)
     if ctx is None:
@@ -418,6 +859,7 @@ def forward(pl: Plan, Q, K, V, O=None, ctx: Context | None = None, ws: Workspace
     _check(LIB.lh_forward(pl.byref(), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(ctx.buf),
                           ctx.buf.numel(), _ptr(ws.buf), ws.buf.numel(), _stream(stream)),
            "lh_forward")
+    ctx.rotary = None if rotary is None else (rotary, positions, start)
     return O, ctx
 
 
@@ -435,6 +877,10 @@ def backward(pl: Plan, dO, ctx: Context, dQ=None, dK=None, dV=None, ws: Workspac
     _check(LIB.lh_backward(pl.byref(), _ptr(dO), _ptr(ctx.buf), ctx.buf.numel(), _ptr(dQ),
                            _ptr(dK), _ptr(dV), _ptr(ws.buf), ws.buf.numel(), _stream(stream)),
            "lh_backward")
+    if ctx.rotary is not None:
+        rp, positions, start = ctx.rotary
+        grads = _bhnd(pl, dQ, dK)
+        _rotate(rp, grads, grads, positions, start, 1, stream)
     return dQ, dK, dV
 
 
