@@ -16,7 +16,7 @@
 // ranges depend on lengths and grid alone: no atomics, no block waits for
 // another.
 //
-// More than max_heads query heads on one key head are cut into parts of equal
+// More query heads on one key head than a block serves are cut into parts of equal
 // size that count as key heads of their own here.
 #include <algorithm>
 
@@ -30,6 +30,7 @@ constexpr int kTile = 64;       // slots of a key tile: the unit of the split
 constexpr int kWarps = 4;       // warps of a block
 constexpr int kDecThreads = kWarps * 32;
 constexpr int kJoinThreads = 128;
+constexpr int kMaxBlocks = 148 * 5;  // ranges at most: every block of a core is resident
 constexpr int kJoinSlots = 2048;  // slots whose weights one join block adds
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -43,7 +44,7 @@ struct DecodeCall {
   float scale;        // scale * log2(e)
   void* o;            // [B, Hq, d]
   float* lse;         // [B, Hq]
-  float* part;        // [blocks][2][gv] rows of d + 2 floats: O, m, l
+  float* part;        // [blocks][2][gv] rows of d + 4 floats: O, m, l
   float* scores;      // [B, Hq, capacity], or null
   const float* weights;
   float* weights_out;
@@ -80,25 +81,374 @@ __device__ __forceinline__ int ranges(const DecodeCall& k, int64_t T) { return (
 __device__ __forceinline__ int64_t range_begin(int64_t c, int64_t T, int W) { return c * T / W; }
 __device__ __forceinline__ int range_of(int64_t tile, int64_t T, int W) { return (int)(((tile + 1) * W - 1) / T); }
 
+// Where a segment (the part of one sequence and key head that lies in a range)
+// stands: its slots j0 .. j1 - 1 and the query heads it serves.
+struct Segment {
+  int b, h;          // sequence, key head
+  int head0, gn;     // first query head, how many
+  int j0, j1;
+};
+
+// A core runs one segment with a block's warps and leaves in shared memory, for
+// each of kParts groups of keys and each head, the unnormalised output, the
+// reference m and the sum l.
+
 // Keys handled by a quad of lanes: lane r*4 + c holds channels of key r (of
 // the eight of a warp tile), in chunks of 16 bytes c, c + 4, ...; it keeps q and
 // the running output of GT heads for those channels, so scores take two
 // shuffles and the outputs none until the end of a segment.  GW warps share a
 // tile where the heads are more than GT.
-template <typename T, int D, int GT, int GW>
-__global__ void __launch_bounds__(kDecThreads)
+template <typename T_, int D_, int GT, int GW>
+struct QuadCore {
+  using T = T_;
+  static constexpr int D = D_, kParts = kWarps / GW, kHeads = GT * GW;
+  static constexpr int kBlocks = D == 64 ? (GT == 1 ? 4 : GT == 2 ? 3 : 2) : (GT == 1 ? 3 : 2);
+  static constexpr int EPC = 16 / sizeof(T);  // elements of a 16-byte chunk
+  static constexpr int NC = D / 4 / EPC;      // chunks of a lane
+
+  static __device__ __forceinline__ void run(const DecodeCall& k, const Segment& s, float (*sm)[kHeads][D + 4]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, c4 = lane & 3;
+    const int kw = warp / GW, hg = warp % GW;
+    const int64_t capacity = (int64_t)k.c.width << k.page_shift;
+    const T* const kp = static_cast<const T*>(k.c.k);
+    const T* const vp = static_cast<const T*>(k.c.v);
+    float q[GT][NC * EPC], o[GT][NC * EPC], m[GT], l[GT];
+#pragma unroll
+    for (int i = 0; i < GT; ++i) {
+      const int g = hg * GT + i;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      const T* p = static_cast<const T*>(k.q.ptr) + s.b * k.q.sb + (int64_t)(s.head0 + min(g, s.gn - 1)) * k.q.sh;
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          q[i][j * EPC + e] = (float)p[(c4 + 4 * j) * EPC + e] * k.scale;
+          o[i][j * EPC + e] = 0.f;
+        }
+      }
+    }
+    for (int t = s.j0 + kw * 8; t < s.j1; t += kParts * 8) {
+      const int j = t + r;
+      bool live = j < s.j1;
+      int64_t page = 0;
+      if (live) {
+        page = k.c.table[s.b * k.c.table_stride + (j >> k.page_shift)];
+        if (page < 0 || page >= k.c.pages) {
+          live = false;
+          if (c4 == 0) atomicOr(k.status, kStatusPage);
+        }
+      }
+      uint4 kc[NC], vc[NC];
+      const int64_t at = (((page * k.c.H + s.h) << k.page_shift) + (j & ((1 << k.page_shift) - 1))) * D;
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
+        if (live) {
+          kc[i] = __ldg(reinterpret_cast<const uint4*>(kp + at) + c4 + 4 * i);
+          vc[i] = __ldg(reinterpret_cast<const uint4*>(vp + at) + c4 + 4 * i);
+        }
+      }
+      float kf[NC * EPC], vf[NC * EPC];
+      const uint32_t* kw_ = reinterpret_cast<const uint32_t*>(kc);
+      const uint32_t* vw_ = reinterpret_cast<const uint32_t*>(vc);
+#pragma unroll
+      for (int i = 0; i < NC * 4; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          kf[2 * i] = __uint_as_float(kw_[i] << 16);
+          kf[2 * i + 1] = __uint_as_float(kw_[i] & 0xffff0000u);
+          vf[2 * i] = __uint_as_float(vw_[i] << 16);
+          vf[2 * i + 1] = __uint_as_float(vw_[i] & 0xffff0000u);
+        } else {
+          kf[i] = __uint_as_float(kw_[i]);
+          vf[i] = __uint_as_float(vw_[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < GT; ++i) {
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < NC * EPC; ++e) x += q[i][e] * kf[e];
+        x += __shfl_xor_sync(0xffffffffu, x, 1);
+        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        const int g = hg * GT + i;
+        if (k.scores && c4 == 0 && g < s.gn && j < s.j1)
+          k.scores[((int64_t)s.b * k.Hq + s.head0 + g) * capacity + j] = live ? x : -INFINITY;
+        if (!live) continue;
+        if (x > m[i] + kSlack) {  // also the first key: m is -inf
+          const float f = exp2f(m[i] - x);
+          m[i] = x;
+          l[i] *= f;
+#pragma unroll
+          for (int e = 0; e < NC * EPC; ++e) o[i][e] *= f;
+        }
+        const float p = exp2f(x - m[i]);
+        l[i] += p;
+#pragma unroll
+        for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * vf[e];
+      }
+    }
+    // Join the eight key rows of the warp.
+#pragma unroll
+    for (int i = 0; i < GT; ++i) {
+      float top = m[i];
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - top);
+      l[i] *= f;
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+      const int g = hg * GT + i;
+#pragma unroll
+      for (int e = 0; e < NC * EPC; ++e) {
+        float v = o[i][e] * f;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
+        if (r == 0) sm[kw][g][(c4 + 4 * (e / EPC)) * EPC + e % EPC] = v;
+      }
+      if (lane == 0) {
+        sm[kw][g][D] = top;
+        sm[kw][g][D + 1] = l[i];
+      }
+    }
+  }
+};
+
+// bf16 on the tensor cores: a warp takes 16 keys, Sᵀ = K Qᵀ and Oᵀ += Vᵀ Pᵀ with
+// mma.m16n8k16, NT groups of eight query heads as the n dimension.  Which keys
+// and channels stand at which index of a contraction is free, so every lane
+// loads its fragments straight from memory, 16 bytes at a time and each byte
+// once:
+//   K  lane (r, c) holds 16-byte chunks c, c + 4, .. of keys r and r + 8: two of
+//      a chunk's four words are an A fragment's k pairs; Q is read alike;
+//   V  it holds chunk r (and r + 8) of keys 2c, 2c + 1, 2c + 8, 2c + 9; a byte
+//      permute pairs two keys of one channel, channels 8r + 2w and + 1 being rows
+//      r and r + 8 of m tile w;
+//   P  the two 8 x 8 halves of Sᵀ become the B fragment by movmatrix.
+// No shared memory is touched until the end of a segment.  K of the next tile is
+// asked for as soon as Sᵀ is formed, V as soon as it is used.  The work is 4 g d
+// flops per 4 d bytes, far below what even this instruction reaches, so it is
+// chosen over tcgen05, whose operands would have to pass through shared
+// memory, for its register operands.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Cache rows are read once: past L1.
+__device__ __forceinline__ uint4 load_row(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+template <int D_, int NT>
+struct MmaCore {
+  using T = __nv_bfloat16;
+  static constexpr int D = D_, kParts = kWarps, kHeads = 8 * NT;
+  static constexpr int kBlocks = D == 64 ? (NT == 1 ? 5 : 4) : (NT == 1 ? 3 : 2);
+  static constexpr int KC = D / 32, VC = D / 64;
+
+  static __device__ __forceinline__ void run(const DecodeCall& k, const Segment& s, float (*sm)[kHeads][D + 4]) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = lane >> 2, c4 = lane & 3;
+    const int64_t capacity = (int64_t)k.c.width << k.page_shift;
+    const int in_page = (1 << k.page_shift) - 1;
+    const int32_t* const table = k.c.table + s.b * k.c.table_stride;
+    const T* const kp = static_cast<const T*>(k.c.k);
+    const T* const vp = static_cast<const T*>(k.c.v);
+
+    uint4 q[NT][KC];
+    float o[NT][VC * 4][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int g = i * 8 + r;
+      const T* p = static_cast<const T*>(k.q.ptr) + s.b * k.q.sb + (int64_t)(s.head0 + min(g, s.gn - 1)) * k.q.sh;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) q[i][j] = __ldg(reinterpret_cast<const uint4*>(p) + c4 + 4 * j);
+#pragma unroll
+      for (int w = 0; w < VC * 4; ++w) o[i][w][0] = o[i][w][1] = o[i][w][2] = o[i][w][3] = 0.f;
+      m[i][0] = m[i][1] = -INFINITY;
+      l[i][0] = l[i][1] = 0.f;
+    }
+
+    // First element of the tile's rows, or -1 where its page is bad.  A tile of
+    // 16 slots lies in one page.
+    auto place = [&](int t) -> int64_t {
+      const int64_t page = table[t >> k.page_shift];
+      if (page < 0 || page >= k.c.pages) {
+        if (lane == 0) atomicOr(k.status, kStatusPage);
+        return -1;
+      }
+      return (((page * k.c.H + s.h) << k.page_shift) + (t & in_page)) * D;
+    };
+    uint4 kc[2][KC], vc[4][VC];
+    auto load_k = [&](int64_t at, int t) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool live = at >= 0 && t + r + 8 * i < s.j1;
+#pragma unroll
+        for (int j = 0; j < KC; ++j)
+          kc[i][j] = live ? load_row(kp + at + (r + 8 * i) * D + (c4 + 4 * j) * 8) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int64_t at, int t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 2 * c4 + (i & 1) + 8 * (i >> 1);
+        const bool live = at >= 0 && t + row < s.j1;
+#pragma unroll
+        for (int j = 0; j < VC; ++j)
+          vc[i][j] = live ? load_row(vp + at + row * D + (r + 8 * j) * 8) : make_uint4(0, 0, 0, 0);
+      }
+    };
+
+    int t = s.j0 + warp * 16;
+    int64_t at = -1;
+    if (t < s.j1) {
+      at = place(t);
+      load_k(at, t);
+      load_v(at, t);
+    }
+    while (t < s.j1) {
+      const int next = t + kWarps * 16;
+      int64_t at_next = -1;
+      if (next < s.j1) at_next = place(next);
+      float x[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {word(kc[0][j], 2 * h), word(kc[1][j], 2 * h), word(kc[0][j], 2 * h + 1),
+                                   word(kc[1][j], 2 * h + 1)};
+            mma16816(x[i], a, word(q[i][j], 2 * h), word(q[i][j], 2 * h + 1));
+          }
+        }
+      }
+      if (next < s.j1) load_k(at_next, next);
+      const bool live0 = at >= 0 && t + r < s.j1, live1 = at >= 0 && t + r + 8 < s.j1;
+      bool grows = false;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[i][e] = (e < 2 ? live0 : live1) ? x[i][e] * k.scale : -INFINITY;
+          grows |= x[i][e] > m[i][e & 1] + kSlack;
+        }
+        if (k.scores) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int g = i * 8 + 2 * c4 + (e & 1), j = t + r + 8 * (e >> 1);
+            if (g < s.gn && j < s.j1) k.scores[((int64_t)s.b * k.Hq + s.head0 + g) * capacity + j] = x[i][e];
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, grows)) {  // the first tile, and then rarely
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(x[i][e], x[i][e + 2]);
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, y));
+            top = fmaxf(top, m[i][e]);
+            const float f = top == -INFINITY ? 1.f : exp2_approx(m[i][e] - top);
+            m[i][e] = top;
+            l[i][e] *= f;
+#pragma unroll
+            for (int w = 0; w < VC * 4; ++w) {
+              o[i][w][e] *= f;
+              o[i][w][e + 2] *= f;
+            }
+          }
+        }
+      }
+      uint32_t p0[NT], p1[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? live0 : live1) ? exp2_approx(x[i][e] - m[i][e & 1]) : 0.f;
+        l[i][0] += p[0] + p[2];
+        l[i][1] += p[1] + p[3];
+        // Rounded to bf16 as an operand: half a step, 2^-8, of each probability.
+        __nv_bfloat162 lo = __floats2bfloat162_rn(p[0], p[1]), hi = __floats2bfloat162_rn(p[2], p[3]);
+        p0[i] = transpose8x8(*reinterpret_cast<uint32_t*>(&lo));
+        p1[i] = transpose8x8(*reinterpret_cast<uint32_t*>(&hi));
+      }
+#pragma unroll
+      for (int j = 0; j < VC; ++j) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a[4] = {__byte_perm(word(vc[0][j], w), word(vc[1][j], w), 0x5410),
+                                 __byte_perm(word(vc[0][j], w), word(vc[1][j], w), 0x7632),
+                                 __byte_perm(word(vc[2][j], w), word(vc[3][j], w), 0x5410),
+                                 __byte_perm(word(vc[2][j], w), word(vc[3][j], w), 0x7632)};
+#pragma unroll
+          for (int i = 0; i < NT; ++i) mma16816(o[i][j * 4 + w], a, p0[i], p1[i]);
+        }
+      }
+      if (next < s.j1) load_v(at_next, next);
+      t = next;
+      at = at_next;
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int g = i * 8 + 2 * c4 + e;
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) l[i][e] += __shfl_xor_sync(0xffffffffu, l[i][e], y);
+#pragma unroll
+        for (int j = 0; j < VC; ++j) {
+          float* p = &sm[warp][g][j * 64 + r * 8];
+#pragma unroll
+          for (int w = 0; w < 4; w += 2)
+            *reinterpret_cast<float4*>(p + 2 * w) =
+                make_float4(o[i][j * 4 + w][e], o[i][j * 4 + w][e + 2], o[i][j * 4 + w + 1][e], o[i][j * 4 + w + 1][e + 2]);
+        }
+        if (r == 0) {
+          sm[warp][g][D] = m[i][e];
+          sm[warp][g][D + 1] = l[i][e];
+        }
+      }
+    }
+  }
+};
+
+// Walks a block's range of tiles, segment by segment.
+template <class Core>
+__global__ void __launch_bounds__(kDecThreads, Core::kBlocks)
 decode_kernel(const __grid_constant__ DecodeCall k) {
-  constexpr int EPC = 16 / sizeof(T);     // elements of a 16-byte chunk
-  constexpr int NC = D / 4 / EPC;         // chunks of a lane
-  constexpr int NW = kWarps / GW;         // warps along the keys
-  __shared__ float sm_o[NW][GT * GW][D + 2];
+  using T = typename Core::T;
+  constexpr int D = Core::D, NP = Core::kParts;
+  __shared__ __align__(16) float sm_o[NP][Core::kHeads][D + 4];
   __shared__ int64_t warp_sums[kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_first;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r = lane >> 2, c4 = lane & 3;
-  const int kw = warp / GW, hg = warp % GW;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int Hv = k.c.H * k.nv;
+  cudaTriggerProgrammaticLaunchCompletion();
 
   int64_t sum = 0;
   for (int b = tid; b < k.c.B; b += kDecThreads) sum += tiles_of(seq_length(k, b));
@@ -106,7 +456,7 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
   const int W = ranges(k, T_all);
   if ((int)blockIdx.x >= W) return;
   int64_t u = range_begin(blockIdx.x, T_all, W);
-  const int64_t u_end = range_begin(blockIdx.x + 1, T_all, W);
+  const int64_t u_begin = u, u_end = range_begin(blockIdx.x + 1, T_all, W);
 
   // The sequence that tile u lies in.
   if (tid < 32) {
@@ -133,9 +483,6 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
   int b = s_b;
   int64_t first = s_first;  // first tile of sequence b
 
-  const int64_t capacity = (int64_t)k.c.width << k.page_shift;
-  const T* const kp = static_cast<const T*>(k.c.k);
-  const T* const vp = static_cast<const T*>(k.c.v);
   while (u < u_end) {
     const int n = seq_length(k, b);
     const int nt = tiles_of(n);
@@ -147,142 +494,47 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
     const int hv = (int)((u - first) / nt);
     const int64_t seg0 = first + (int64_t)hv * nt, seg1 = seg0 + nt;
     const int64_t stop = min(seg1, u_end);
-    const int h = hv / k.nv, part = hv % k.nv;
-    const int g0 = part * k.gv, gn = min(k.gv, k.G - g0);  // query heads g0 .. of the group
-    const int head0 = h * k.G + g0;
-
-    float q[GT][NC * EPC], o[GT][NC * EPC], m[GT], l[GT];
-#pragma unroll
-    for (int i = 0; i < GT; ++i) {
-      const int g = hg * GT + i;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      const T* p = static_cast<const T*>(k.q.ptr) + b * k.q.sb + (int64_t)(head0 + min(g, gn - 1)) * k.q.sh;
-#pragma unroll
-      for (int j = 0; j < NC; ++j) {
-#pragma unroll
-        for (int e = 0; e < EPC; ++e) {
-          q[i][j * EPC + e] = (float)p[(c4 + 4 * j) * EPC + e] * k.scale;
-          o[i][j * EPC + e] = 0.f;
-        }
-      }
-    }
-    const int j0 = (int)(u - seg0) * kTile, j1 = min(n, (int)(stop - seg0) * kTile);
-    for (int t = j0 + kw * 8; t < j1; t += NW * 8) {
-      const int j = t + r;
-      bool live = j < j1;
-      int64_t page = 0;
-      if (live) {
-        page = k.c.table[b * k.c.table_stride + (j >> k.page_shift)];
-        if (page < 0 || page >= k.c.pages) {
-          live = false;
-          if (c4 == 0) atomicOr(k.status, kStatusPage);
-        }
-      }
-      uint4 kc[NC], vc[NC];
-      const int64_t at = (((page * k.c.H + h) << k.page_shift) + (j & ((1 << k.page_shift) - 1))) * D;
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-        if (live) {
-          kc[i] = __ldg(reinterpret_cast<const uint4*>(kp + at) + c4 + 4 * i);
-          vc[i] = __ldg(reinterpret_cast<const uint4*>(vp + at) + c4 + 4 * i);
-        }
-      }
-      float kf[NC * EPC], vf[NC * EPC];
-      const uint32_t* kw_ = reinterpret_cast<const uint32_t*>(kc);
-      const uint32_t* vw_ = reinterpret_cast<const uint32_t*>(vc);
-#pragma unroll
-      for (int i = 0; i < NC * 4; ++i) {
-        if constexpr (sizeof(T) == 2) {
-          kf[2 * i] = __uint_as_float(kw_[i] << 16);
-          kf[2 * i + 1] = __uint_as_float(kw_[i] & 0xffff0000u);
-          vf[2 * i] = __uint_as_float(vw_[i] << 16);
-          vf[2 * i + 1] = __uint_as_float(vw_[i] & 0xffff0000u);
-        } else {
-          kf[i] = __uint_as_float(kw_[i]);
-          vf[i] = __uint_as_float(vw_[i]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < GT; ++i) {
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < NC * EPC; ++e) s += q[i][e] * kf[e];
-        s += __shfl_xor_sync(0xffffffffu, s, 1);
-        s += __shfl_xor_sync(0xffffffffu, s, 2);
-        const int g = hg * GT + i;
-        if (k.scores && c4 == 0 && g < gn && j < j1)
-          k.scores[((int64_t)b * k.Hq + head0 + g) * capacity + j] = live ? s : -INFINITY;
-        if (!live) continue;
-        if (s > m[i] + kSlack) {  // also the first key: m is -inf
-          const float f = exp2f(m[i] - s);
-          m[i] = s;
-          l[i] *= f;
-#pragma unroll
-          for (int e = 0; e < NC * EPC; ++e) o[i][e] *= f;
-        }
-        const float p = exp2f(s - m[i]);
-        l[i] += p;
-#pragma unroll
-        for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * vf[e];
-      }
-    }
-    // Join the eight key rows of the warp, then the warps along the keys.
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < GT; ++i) {
-      float top = m[i];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - top);
-      l[i] *= f;
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-      const int g = hg * GT + i;
-#pragma unroll
-      for (int e = 0; e < NC * EPC; ++e) {
-        float v = o[i][e] * f;
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(0xffffffffu, v, x);
-        if (r == 0) sm_o[kw][g][(c4 + 4 * (e / EPC)) * EPC + e % EPC] = v;
-      }
-      if (lane == 0) {
-        sm_o[kw][g][D] = top;
-        sm_o[kw][g][D + 1] = l[i];
-      }
-    }
+    Segment s;
+    s.b = b;
+    s.h = hv / k.nv;
+    const int g0 = hv % k.nv * k.gv;
+    s.gn = min(k.gv, k.G - g0);
+    s.head0 = s.h * k.G + g0;
+    s.j0 = (int)(u - seg0) * kTile;
+    s.j1 = (int)min((int64_t)n, (stop - seg0) * kTile);
+    Core::run(k, s, sm_o);
     __syncthreads();
     const bool whole = u == seg0 && stop == seg1;
     // The segment that begins the range leaves its part in slot 0, one that
     // begins inside it and goes on behind it in slot 1.
-    const int slot = u == range_begin(blockIdx.x, T_all, W) ? 0 : 1;
-    float* part_out = k.part + ((int64_t)blockIdx.x * 2 + slot) * k.gv * (D + 2);
-    for (int i = tid; i < gn * D; i += kDecThreads) {
+    const int slot = u == u_begin ? 0 : 1;
+    float* part_out = k.part + ((int64_t)blockIdx.x * 2 + slot) * k.gv * (D + 4);
+    for (int i = tid; i < s.gn * D; i += kDecThreads) {
       const int g = i / D, e = i % D;
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, sm_o[w][g][D]);
+      for (int w = 0; w < NP; ++w) top = fmaxf(top, sm_o[w][g][D]);
       float acc = 0.f, tot = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
+      for (int w = 0; w < NP; ++w) {
         const float mw = sm_o[w][g][D];
         const float f = mw == -INFINITY ? 0.f : exp2f(mw - top);
         acc += f * sm_o[w][g][e];
         tot += f * sm_o[w][g][D + 1];
       }
       if (whole) {
-        const int64_t row = (int64_t)b * k.Hq + head0 + g;
+        const int64_t row = (int64_t)b * k.Hq + s.head0 + g;
         static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? acc / tot : 0.f);
         if (e == 0) k.lse[row] = tot > 0.f ? (top + log2f(tot)) * kLn2 : -INFINITY;
       } else {
-        part_out[g * (D + 2) + e] = acc;
+        part_out[g * (D + 4) + e] = acc;
         if (e == 0) {
-          part_out[g * (D + 2) + D] = top;
-          part_out[g * (D + 2) + D + 1] = tot;
+          part_out[g * (D + 4) + D] = top;
+          part_out[g * (D + 4) + D + 1] = tot;
         }
       }
     }
+    __syncthreads();
     u = stop;
   }
 }
@@ -290,12 +542,15 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
 // Joins the parts of one query head (blockIdx.y = 0 writes O and lse) and adds
 // the probabilities of kJoinSlots slots to the weights of its key head.
 // Without weights the grid is (B * Hq); with them (B * H, slot blocks) and the
-// block goes over the group's heads.
+// block goes over the group's heads.  Launched while decode_kernel still runs:
+// what it needs of lengths and ranges is worked out before the wait.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
-  __shared__ int64_t warp_sums[kJoinThreads / 32];
-  const int tid = threadIdx.x;
+  constexpr int NW = kJoinThreads / 32, E = D / 32;
+  __shared__ int64_t warp_sums[NW];
+  __shared__ float s_f[kMaxBlocks], s_red[NW], s_acc[NW][D];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_b = with_weights ? k.c.H : k.Hq;
   const int b = blockIdx.x / per_b;
   const int head_first = with_weights ? (blockIdx.x % per_b) * k.G : blockIdx.x % per_b;
@@ -320,6 +575,7 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
   const int64_t first = block_sum<kJoinThreads>(before, warp_sums) * Hv;
   const int nt = tiles_of(n);
   const int W = ranges(k, T_all);
+  cudaGridDependencySynchronize();
 
   constexpr int kPer = kJoinSlots / kJoinThreads;
   float add[kPer];
@@ -341,24 +597,62 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
     if (c0 == c1) {
       lse2 = k.lse[row] * kLog2e;
     } else {
-      const int64_t stride = (int64_t)k.gv * (D + 2);
-      const int64_t base = (int64_t)(g % k.gv) * (D + 2);
-      const int late = range_begin(c0, T_all, W) < seg0;  // range c0 holds another segment before
+      // Part c - c0: slot 0 of range c, or slot 1 of range c0 where that holds
+      // another segment before.
+      const int64_t stride = (int64_t)k.gv * (D + 4);
+      const int late = range_begin(c0, T_all, W) < seg0;
+      const float* base = k.part + (int64_t)c0 * 2 * stride + (int64_t)(g % k.gv) * (D + 4);
+      const int parts = c1 - c0 + 1;
+      auto part = [&](int c) { return base + (2 * (int64_t)c + (c == 0 ? late : 0)) * stride; };
       float top = -INFINITY;
-      for (int c = c0; c <= c1; ++c)
-        top = fmaxf(top, k.part[(2 * (int64_t)c + (c == c0 ? late : 0)) * stride + base + D]);
-      float tot = 0.f, acc = 0.f;
-      for (int c = c0; c <= c1; ++c) {
-        const float* p = k.part + (2 * (int64_t)c + (c == c0 ? late : 0)) * stride + base;
-        const float f = p[D] == -INFINITY ? 0.f : exp2f(p[D] - top);
-        tot += f * p[D + 1];
-        if (blockIdx.y == 0 && tid < D) acc += f * p[tid];
+      for (int c = tid; c < parts; c += kJoinThreads) {
+        s_f[c] = part(c)[D];
+        top = fmaxf(top, s_f[c]);
       }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      if (lane == 0) s_red[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, s_red[w]);
+      __syncthreads();
+      float tot = 0.f;
+      for (int c = tid; c < parts; c += kJoinThreads) {
+        const float f = s_f[c] == -INFINITY ? 0.f : exp2f(s_f[c] - top);
+        s_f[c] = f;
+        tot += f * part(c)[D + 1];
+      }
+#pragma unroll
+      for (int x = 16; x; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
+      if (lane == 0) s_red[warp] = tot;
+      __syncthreads();
+      tot = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) tot += s_red[w];
       lse2 = top + log2f(tot);
       if (blockIdx.y == 0) {
-        if (tid < D) static_cast<T*>(k.o)[row * D + tid] = (T)(tot > 0.f ? acc / tot : 0.f);
+        float acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int c = warp; c < parts; c += NW) {
+          const float f = s_f[c];
+          const float* p = part(c);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += f * p[lane + 32 * e];
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+        __syncthreads();
+        for (int e = tid; e < D; e += kJoinThreads) {
+          float v = 0.f;
+#pragma unroll
+          for (int w = 0; w < NW; ++w) v += s_acc[w][e];
+          static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? v / tot : 0.f);
+        }
         if (tid == 0) k.lse[row] = tot > 0.f ? lse2 * kLn2 : -INFINITY;
       }
+      __syncthreads();
     }
     if (with_weights) {
       const float* s = k.scores + row * capacity;
@@ -382,9 +676,31 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
   }
 }
 
-// Query heads that one block serves: GT * GW of decode_kernel's widest form, as
-// many as its registers hold.
-constexpr int max_heads(int d) { return d == 64 ? 16 : 8; }
+// Calls f.template operator()<Core>() for the core that serves gv query heads a
+// key head.
+template <typename F>
+void with_core(int dtype, int d, int gv, F&& f) {
+  if (dtype == LH_BF16) {
+    if (d == 64) {
+      if (gv <= 8) f.template operator()<MmaCore<64, 1>>();
+      else f.template operator()<MmaCore<64, 2>>();
+    } else {
+      if (gv <= 8) f.template operator()<MmaCore<128, 1>>();
+      else f.template operator()<MmaCore<128, 2>>();
+    }
+  } else if (d == 64) {
+    if (gv == 1) f.template operator()<QuadCore<float, 64, 1, 1>>();
+    else if (gv == 2) f.template operator()<QuadCore<float, 64, 2, 1>>();
+    else if (gv <= 4) f.template operator()<QuadCore<float, 64, 2, 2>>();
+    else if (gv <= 8) f.template operator()<QuadCore<float, 64, 2, 4>>();
+    else f.template operator()<QuadCore<float, 64, 4, 4>>();
+  } else {
+    if (gv == 1) f.template operator()<QuadCore<float, 128, 1, 1>>();
+    else if (gv == 2) f.template operator()<QuadCore<float, 128, 2, 1>>();
+    else if (gv <= 4) f.template operator()<QuadCore<float, 128, 2, 2>>();
+    else f.template operator()<QuadCore<float, 128, 2, 4>>();
+  }
+}
 
 struct Sizes {
   int nv, gv, blocks;
@@ -394,21 +710,18 @@ struct Sizes {
 Sizes sizes(const lh_cache& c, int64_t Hq, bool with_weights) {
   Sizes s{};
   const int64_t G = Hq / c.H;
-  const int most_heads = max_heads(c.d);
+  // Query heads that one block serves at most: 16, or 8 where an fp32 row of 128
+  // channels leaves registers for no more.
+  const int most_heads = c.dtype == LH_F32 && c.d == 128 ? 8 : 16;
   s.nv = (int)((G + most_heads - 1) / most_heads);
   s.gv = (int)((G + s.nv - 1) / s.nv);
   s.nv = (int)((G + s.gv - 1) / s.gv);
   const int64_t capacity = (int64_t)c.width * c.page;
   const int64_t most = (int64_t)c.B * c.H * s.nv * ((capacity + kTile - 1) / kTile);
-  s.blocks = (int)std::min<int64_t>(most, 148 * 4);
-  s.part = ((int64_t)s.blocks * 2 * s.gv * (c.d + 2) * 4 + 255) & ~int64_t(255);
+  with_core(c.dtype, c.d, s.gv, [&]<typename Core>() { s.blocks = (int)std::min<int64_t>(most, 148 * Core::kBlocks); });
+  s.part = ((int64_t)s.blocks * 2 * s.gv * (c.d + 4) * 4 + 255) & ~int64_t(255);
   s.scores = with_weights ? (int64_t)c.B * Hq * capacity * 4 : 0;
   return s;
-}
-
-template <typename T, int D, int GT, int GW>
-void run(const DecodeCall& k, cudaStream_t st) {
-  decode_kernel<T, D, GT, GW><<<k.blocks, kDecThreads, 0, st>>>(k);
 }
 
 }  // namespace
@@ -440,19 +753,24 @@ cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void
   k.nv = z.nv;
   k.gv = z.gv;
   k.blocks = z.blocks;
-  with_type_dim(c.dtype, c.d, [&]<typename T, int D>() {
-    if (k.gv == 1) run<T, D, 1, 1>(k, st);
-    else if (k.gv == 2) run<T, D, 2, 1>(k, st);
-    else if (k.gv <= 4) run<T, D, 2, 2>(k, st);
-    else if (k.gv <= 8) run<T, D, 2, 4>(k, st);
-    else if constexpr (D == 64) run<T, D, 4, 4>(k, st);
-    cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  with_core(c.dtype, c.d, k.gv, [&]<typename Core>() {
+    decode_kernel<Core><<<k.blocks, kDecThreads, 0, st>>>(k);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return;
     const int64_t capacity = (int64_t)c.width * c.page;
-    const dim3 grid(ww ? c.B * c.H : c.B * Q.H, ww ? (unsigned)((capacity + kJoinSlots - 1) / kJoinSlots) : 1);
-    join_kernel<T, D><<<grid, kJoinThreads, 0, st>>>(k, ww);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ww ? c.B * c.H : c.B * Q.H, ww ? (unsigned)((capacity + kJoinSlots - 1) / kJoinSlots) : 1);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute overlap{};
+    overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &overlap;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, join_kernel<typename Core::T, Core::D>, k, ww);
   });
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace lh
