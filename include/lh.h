@@ -293,6 +293,7 @@ typedef struct {
 typedef struct {
   lh_rotary_config c;
   uint64_t turns[LH_MAX_PAIRS];
+  uint64_t check; /* set by lh_rotary_init; the calls refuse a plan it does not fit */
 } lh_rotary_plan;
 
 /* Fill *out from *cfg.  Host only.  LH_ERR_INVALID_ARG: rot not in 1..d,

@@ -73,7 +73,8 @@ class LhRotaryConfig(ctypes.Structure):
 
 
 class LhRotaryPlan(ctypes.Structure):
-    _fields_ = [("c", LhRotaryConfig), ("turns", ctypes.c_uint64 * MAX_PAIRS)]
+    _fields_ = [("c", LhRotaryConfig), ("turns", ctypes.c_uint64 * MAX_PAIRS),
+                ("check", ctypes.c_uint64)]
 
 
 class LhRows(ctypes.Structure):
@@ -402,6 +403,12 @@ def gather_bwd(pl: Plan, dQg, dKg, dVg, slot_of, stream=None):
 # --- rotary positions ---------------------------------------------------------
 
 
+# The device's current stream as an integer handle (a Stream object costs more
+# to make than a small call takes on the GPU).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _run(dev, stream, inputs, call):
     """``call(handle)`` enqueues on ``stream`` (default: the device's current one)
     and returns the tensors it allocated, with ``dev`` as the current device.
@@ -409,16 +416,18 @@ def _run(dev, stream, inputs, call):
     On a stream other than the current one the outputs come from that stream's
     memory pool, and every tensor is recorded on the stream it is used on next
     to its own, so that none is handed out again while the other one works."""
-    cur = torch.cuda.current_stream(dev)
-    if stream is None or stream == cur:
+    if stream is None:
         if dev.index == torch.cuda.current_device():
-            return call(ctypes.c_void_p(cur.cuda_stream))
+            return call(_raw_stream(dev.index))
         with torch.cuda.device(dev):
-            return call(ctypes.c_void_p(cur.cuda_stream))
+            return call(_raw_stream(dev.index))
+    cur = torch.cuda.current_stream(dev)
+    if stream == cur:
+        return _run(dev, None, inputs, call)
     if stream.device != dev:
         raise ValueError(f"stream: on {stream.device}, the tensors are on {dev}")
     with torch.cuda.stream(stream):
-        outs = call(ctypes.c_void_p(stream.cuda_stream))
+        outs = call(stream.cuda_stream)
     for t in inputs:
         if t is not None:
             t.record_stream(stream)
@@ -428,12 +437,14 @@ def _run(dev, stream, inputs, call):
     return outs
 
 
-def _on_device(dev, **tensors):
+def _on_device(dev, names, tensors):
+    """All tensors of the call (those that are not None) are on the CUDA device ``dev``."""
     if dev.type != "cuda":
-        raise ValueError(f"{next(iter(tensors))}: must be a CUDA tensor (got {dev})")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, the call runs on {dev}")
+        raise ValueError(f"{names.split()[0]}: must be a CUDA tensor (got {dev})")
+    index = dev.index
+    for i, t in enumerate(tensors):
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{names.split()[i]}: on {t.device}, the call runs on {dev}")
 
 
 def _strided(t, name: str, dtype, shape):
@@ -442,16 +453,25 @@ def _strided(t, name: str, dtype, shape):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 4 or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+    have = t.shape
+    if len(have) != 4 or have[0] != shape[0] or have[2] != shape[2] or have[3] != shape[3] or \
+            (shape[1] is not None and have[1] != shape[1]):
         want = ", ".join("*" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{want}]")
+        raise ValueError(f"{name}: shape {tuple(have)}, expected [{want}]")
     if t.stride(3) != 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
 
 
-def _lh_rows(t):
-    s = t.stride()
-    return LhRows(t.data_ptr(), s[0], s[1], s[2], t.shape[1])
+_ROWS = [None] + [_I64 * (5 * n) for n in (1, 2)]
+
+
+def _lh_rows(*tensors):
+    """One or two lh_rows (five 64-bit fields each) as a flat array."""
+    flat = []
+    for t in tensors:
+        sb, sh, sn, _ = t.stride()
+        flat += (t.data_ptr(), sb, sh, sn, t.shape[1])
+    return _ROWS[len(tensors)](*flat)
 
 
 def _index(t, name: str, shape):
@@ -460,7 +480,7 @@ def _index(t, name: str, shape):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != torch.int32:
         raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -507,6 +527,11 @@ def rotary_plan(d: int = 64, rot: int | None = None, base: float = 10000.0, layo
     return RotaryPlan(raw)
 
 
+def _contiguous_like(t):
+    return torch.empty_like(t) if t.is_contiguous() else \
+        torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _rotate(rp: RotaryPlan, X, Y, positions, start, transpose, stream):
     """Turn the one or two tensors X into Y (None: new contiguous tensors)."""
     first = X[0]
@@ -515,27 +540,24 @@ def _rotate(rp: RotaryPlan, X, Y, positions, start, transpose, stream):
     if first.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"Q: dtype {first.dtype}, expected torch.bfloat16 or torch.float32")
     B, _, N, _ = first.shape
-    named = dict(zip(("Q", "K"), X))
-    for name, t in named.items():
-        _strided(t, name, first.dtype, (B, None, N, rp.d))
-    if Y is not None:
-        for x, (name, t) in zip(X, zip(("out[0]", "out[1]"), Y)):
-            _strided(t, name, first.dtype, x.shape)
-            named[name] = t
-    stride = _positions(positions, B, N)
+    shape = (B, None, N, rp.raw.c.d)
+    for i, t in enumerate(X):
+        _strided(t, "QK"[i], first.dtype, shape)
+        if Y is not None:
+            _strided(Y[i], f"out[{i}]", first.dtype, t.shape)
+    stride = 0 if positions is None else _positions(positions, B, N)
     dev = first.device
-    _on_device(dev, **named, positions=positions)
+    tensors = (*X, positions) if Y is None else (*X, positions, *Y)
+    _on_device(dev, "Q positions out" if len(X) == 1 else "Q K positions out[0] out[1]", tensors)
 
     def call(handle):
-        out = tuple(torch.empty(x.shape, dtype=x.dtype, device=dev) for x in X) if Y is None else Y
-        n = len(X)
-        xs, ys = (LhRows * n)(*map(_lh_rows, X)), (LhRows * n)(*map(_lh_rows, out))
-        if first.numel() or X[-1].numel():
-            _check(LIB.lh_rotary(ctypes.byref(rp.raw), _dtype_code(first), B, N, n, xs, ys, _ptr(positions),
-                                 stride, start, transpose, handle), "lh_rotary")
+        out = tuple([_contiguous_like(x) for x in X]) if Y is None else Y
+        if B and N:
+            _check(LIB.lh_rotary(ctypes.byref(rp.raw), _dtype_code(first), B, N, len(X), _lh_rows(*X),
+                                 _lh_rows(*out), _ptr(positions), stride, start, transpose, handle), "lh_rotary")
         return out
 
-    return _run(dev, stream, (*X, positions), call)
+    return _run(dev, stream, tensors, call)
 
 
 def _pair(Q, K, out):
@@ -597,6 +619,7 @@ class PagedCache:
             raise ValueError(f"v: on {v.device}, k on {k.device}")
         self.k, self.v = k, v
         self.pages, self.H, self.page, self.d = k.shape
+        self._c = LhCache(k.data_ptr(), v.data_ptr(), *k.shape, _dtype_code(k))
 
     @property
     def dtype(self):
@@ -612,9 +635,10 @@ class PagedCache:
         if width > 1 and table.stride(1) != 1:
             raise ValueError("table: a sequence's pages must be contiguous")
         _index(lengths, "lengths", (B,))
-        return LhCache(self.k.data_ptr(), self.v.data_ptr(), self.pages, self.H, self.page, self.d,
-                       _dtype_code(self.k), table.data_ptr(), table.stride(0), B, width,
-                       lengths.data_ptr()), B, width * self.page
+        raw = LhCache.from_buffer_copy(self._c)
+        raw.table, raw.table_stride, raw.B, raw.width = table.data_ptr(), table.stride(0), B, width
+        raw.lengths = lengths.data_ptr()
+        return raw, B, width * self.page
 
 
 def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: RotaryPlan | None = None,
@@ -632,17 +656,16 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
     raw, B, capacity = cache._raw(table, lengths)
     T = K.shape[2]
     shape = (B, cache.H, T, cache.d)
-    named = {"K": K, "V": V, "table": table, "lengths": lengths, "positions": positions,
-             "counts": counts, "slot_positions": slot_positions, "Q": Q, "out": out}
-    for name in ("K", "V"):
-        _strided(named[name], name, cache.dtype, shape)
+    dtype = cache.k.dtype
+    _strided(K, "K", dtype, shape)
+    _strided(V, "V", dtype, shape)
     if Q is not None:
-        _strided(Q, "Q", cache.dtype, (B, None, T, cache.d))
+        _strided(Q, "Q", dtype, (B, None, T, cache.d))
         if out is not None:
-            _strided(out, "out", cache.dtype, Q.shape)
+            _strided(out, "out", dtype, Q.shape)
     elif out is not None:
         raise ValueError("out: given without Q")
-    stride = _positions(positions, B, T)
+    stride = 0 if positions is None else _positions(positions, B, T)
     if counts is not None:
         _index(counts, "counts", (B,))
     if slot_positions is not None:
@@ -650,20 +673,19 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
     if rotary is not None and rotary.d != cache.d:
         raise ValueError(f"rotary: for d = {rotary.d}, the cache has d = {cache.d}")
     dev = cache.k.device
-    _on_device(dev, cache=cache.k, **named)
+    tensors = (cache.k, cache.v, K, V, table, lengths, positions, counts, slot_positions, Q, out)
+    _on_device(dev, "cache cache K V table lengths positions counts slot_positions Q out", tensors)
 
     def call(handle):
-        qo = out
-        if Q is not None and out is None:
-            qo = torch.empty(Q.shape, dtype=Q.dtype, device=dev)
+        qo = _contiguous_like(Q) if Q is not None and out is None else out
         if T and B:
-            rows = [None if t is None else ctypes.byref(_lh_rows(t)) for t in (K, V, Q, qo)]
             _check(LIB.lh_cache_append(ctypes.byref(raw), None if rotary is None else ctypes.byref(rotary.raw),
-                                       T, *rows, _ptr(positions), stride, _ptr(counts), _ptr(slot_positions),
-                                       handle), "lh_cache_append")
+                                       T, _lh_rows(K), _lh_rows(V), None if Q is None else _lh_rows(Q),
+                                       None if Q is None else _lh_rows(qo), _ptr(positions), stride,
+                                       _ptr(counts), _ptr(slot_positions), handle), "lh_cache_append")
         return (qo,)
 
-    return _run(dev, stream, (*named.values(), cache.k, cache.v), call)[0]
+    return _run(dev, stream, tensors, call)[0]
 
 
 def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, weights=None,
@@ -677,7 +699,7 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
     ws: a uint8 scratch tensor of decode_ws_bytes(); calls that overlap on the
     GPU need one each (default: a new one)."""
     raw, B, capacity = cache._raw(table, lengths)
-    _strided(Q, "Q", cache.dtype, (B, None, 1, cache.d))
+    _strided(Q, "Q", cache.k.dtype, (B, None, 1, cache.d))
     Hq = Q.shape[1]
     if weights is None and weights_out is not None:
         raise ValueError("weights_out: given without weights")
@@ -691,21 +713,19 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
                     "lh_decode_ws_bytes", B)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
-    _on_device(dev, cache=cache.k, table=table, lengths=lengths, Q=Q, weights=weights,
-               weights_out=weights_out, ws=ws)
+    tensors = (cache.k, cache.v, table, lengths, Q, weights, weights_out, ws)
+    _on_device(dev, "cache cache table lengths Q weights weights_out ws", tensors)
 
     def call(handle):
-        o = torch.empty((B, Hq, 1, cache.d), dtype=Q.dtype, device=dev)
+        o = _contiguous_like(Q)
         lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=dev)
         w = _bytes(need, dev) if ws is None else ws
         if B:
-            q = _lh_rows(Q)
-            _check(LIB.lh_decode(ctypes.byref(raw), ctypes.byref(q),
-                                 cache.d ** -0.5 if scale is None else scale, _ptr(o), _ptr(lse), _ptr(weights),
-                                 _ptr(weights_out), _ptr(w), w.numel(), handle), "lh_decode")
+            _check(LIB.lh_decode(ctypes.byref(raw), _lh_rows(Q), cache.d ** -0.5 if scale is None else scale,
+                                 _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.numel(), handle), "lh_decode")
         return o, lse
 
-    return _run(dev, stream, (cache.k, cache.v, table, lengths, Q, weights, weights_out, ws), call)
+    return _run(dev, stream, tensors, call)
 
 
 def _slots(t, name: str, dtype, shape):
@@ -713,7 +733,7 @@ def _slots(t, name: str, dtype, shape):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -762,23 +782,20 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
     need = _ws_need(LIB.lh_evict_ws_bytes(ctypes.byref(raw), budget), "lh_evict_ws_bytes", B)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
-    _on_device(dev, cache=cache.k, table=table, lengths=lengths, weights=weights, weights_out=weights_out,
-               positions=positions, positions_out=positions_out, protect=protect, ws=ws)
+    tensors = (cache.k, cache.v, table, lengths, weights, weights_out, positions, positions_out, protect, ws)
+    _on_device(dev, "cache cache table lengths weights weights_out positions positions_out protect ws", tensors)
 
     def call(handle):
-        n = torch.empty((B,), dtype=torch.int32, device=dev)
-        wo = torch.empty(shape, dtype=torch.float32, device=dev) if weights_out is None else weights_out
-        po = positions_out
-        if positions is not None and po is None:
-            po = torch.empty(shape, dtype=torch.int32, device=dev)
+        n = torch.empty_like(lengths)
+        wo = torch.empty_like(weights) if weights_out is None else weights_out
+        po = torch.empty_like(positions) if positions is not None and positions_out is None else positions_out
         w = _bytes(need, dev) if ws is None else ws
         if B:
             _check(LIB.lh_evict(ctypes.byref(raw), budget, _ptr(weights), _ptr(positions), _ptr(protect),
                                 _ptr(wo), _ptr(po), _ptr(n), _ptr(w), w.numel(), handle), "lh_evict")
         return n, wo, po
 
-    return _run(dev, stream, (cache.k, cache.v, table, lengths, weights, weights_out, positions, positions_out,
-                              protect, ws), call)
+    return _run(dev, stream, tensors, call)
 
 
 def evict_ws_bytes(cache: PagedCache, table, lengths, budget: int) -> int:
