@@ -31,7 +31,7 @@ constexpr int kWarps = 4;       // warps of a block
 constexpr int kDecThreads = kWarps * 32;
 constexpr int kJoinThreads = 128;
 constexpr int kMaxBlocks = 148 * 5;  // ranges at most: every block of a core is resident
-constexpr int kJoinSlots = 2048;  // slots whose weights one join block adds
+constexpr int kJoinSlots = 512;   // slots whose weights one join block adds, four a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A warp keeps its running reference until a score passes it by this many
@@ -575,12 +575,13 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
   const int64_t first = block_sum<kJoinThreads>(before, warp_sums) * Hv;
   const int nt = tiles_of(n);
   const int W = ranges(k, T_all);
+  static_assert(kJoinSlots == 4 * kJoinThreads, "four slots a thread");
+  const int j0 = slot0 + tid * 4;
+  float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (with_weights && j0 < n)
+    add = *reinterpret_cast<const float4*>(k.weights + ((int64_t)b * k.c.H + head_first / k.G) * capacity + j0);
   cudaGridDependencySynchronize();
 
-  constexpr int kPer = kJoinSlots / kJoinThreads;
-  float add[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) add[i] = 0.f;
   for (int i = 0; i < heads; ++i) {
     const int head = head_first + i;
     const int64_t row = (int64_t)b * k.Hq + head;
@@ -654,24 +655,23 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
       }
       __syncthreads();
     }
-    if (with_weights) {
-      const float* s = k.scores + row * capacity;
-#pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const int j = slot0 + x * kJoinThreads + tid;
-        if (j < n) {
-          const float v = s[j];
-          add[x] += v == -INFINITY ? 0.f : exp2f(v - lse2);
-        }
-      }
+    if (with_weights && j0 < n) {
+      // Slots from n on hold nothing: their sums are not stored.
+      const float4 s = *reinterpret_cast<const float4*>(k.scores + row * capacity + j0);
+      add.x += s.x == -INFINITY ? 0.f : exp2f(s.x - lse2);
+      add.y += s.y == -INFINITY ? 0.f : exp2f(s.y - lse2);
+      add.z += s.z == -INFINITY ? 0.f : exp2f(s.z - lse2);
+      add.w += s.w == -INFINITY ? 0.f : exp2f(s.w - lse2);
     }
   }
-  if (with_weights) {
-    const int64_t row = ((int64_t)b * k.c.H + head_first / k.G) * capacity;
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int j = slot0 + x * kJoinThreads + tid;
-      if (j < n) k.weights_out[row + j] = k.weights[row + j] + add[x];
+  if (with_weights && j0 < n) {
+    float* out = k.weights_out + ((int64_t)b * k.c.H + head_first / k.G) * capacity + j0;
+    if (j0 + 4 <= n) {
+      *reinterpret_cast<float4*>(out) = add;
+    } else {
+      out[0] = add.x;
+      if (j0 + 1 < n) out[1] = add.y;
+      if (j0 + 2 < n) out[2] = add.z;
     }
   }
 }

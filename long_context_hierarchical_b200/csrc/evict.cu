@@ -5,8 +5,9 @@
 // those equal to it the lowest slots.  The m-th largest is found digit by digit
 // (11 + 11 + 10 bits) with histograms in shared memory.  A cluster of blocks
 // shares a head: each keeps the keys of its slots in shared memory, reads the
-// weights once, and adds up the others' histograms and counts over distributed
-// shared memory, so the whole selection is one launch.
+// weights once, adds up its share of the bins over all histograms by distributed
+// shared memory, and reads the share that holds the rank from its owner, so the
+// whole selection is one launch.
 //
 // Rows are not packed in their order: kept rows below slot m stay, and only
 // those from m on move, into the slots given up below m.  Sources and targets are
@@ -28,12 +29,12 @@ namespace cg = cooperative_groups;
 namespace lh {
 namespace {
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kBins = 2048;
-constexpr int kPerThread = 4;
+constexpr int kPerThread = 8;
 constexpr int kSweep = kEvThreads * kPerThread;  // slots of one step of the scan
 constexpr int kMaxCluster = 8;
-constexpr int kHists = 4;  // protected and other rows of the first digit, second, third
+constexpr int kHists = 4;  // other and protected rows of the first digit, second, third
 // Keys (4 bytes) and protection bits of a block's slots in shared memory; a
 // block with more slots reads the weights again in every pass.
 constexpr int kMaxKeys = 40960;
@@ -48,7 +49,7 @@ struct EvictCall {
   int32_t* count;               // [B * H] moves
   int32_t *from, *to;           // [B * H, most]
   float* moved_weight;          // [B * H, most]: the sources' weight and position,
-  int32_t* moved_position;      // whose own entries the scan clears
+  int32_t* moved_position;      // whose own entries the scan clears; sources last first
   unsigned int* status;
   int page_shift;
   int keys;                     // slots whose keys fit the block's shared memory
@@ -61,45 +62,42 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t scan_excl(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+// Sums of the values of the threads before this one, and of all.
+template <typename V>
+__device__ __forceinline__ V scan_excl(V v, V* warp_sums, V* total) {
+  constexpr int NW = kEvThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t x = v;
+  V x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+    const V y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    uint32_t w = warp_sums[lane];
+  V w = lane < NW ? warp_sums[lane] : 0;  // every warp adds up the warps for itself
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    warp_sums[lane] = w;
+  for (int o = 1; o < NW; o <<= 1) {
+    const V y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
+  *total = __shfl_sync(0xffffffffu, w, NW - 1);
+  const V before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   __syncthreads();
-  const uint32_t before = warp == 0 ? 0 : warp_sums[warp - 1];
-  *total = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
+  return (warp == 0 ? 0 : before) + x - v;
 }
 
-struct Counts {
-  uint32_t above, equal, above_m, equal_m;  // of a block's slots, and of those below m
-};
-
-__global__ void __launch_bounds__(kEvThreads)
+__global__ void __launch_bounds__(kEvThreads, 2)
 evict_select_kernel(const __grid_constant__ EvictCall k) {
-  extern __shared__ uint32_t dyn[];
+  extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* const keys = dyn;                     // [k.keys]
   uint32_t* const bits = dyn + k.keys;            // [k.keys / 32] protected
-  __shared__ uint32_t hist[kHists][kBins];
-  __shared__ uint32_t warp_sums[32];
+  __shared__ __align__(16) uint32_t hist[kHists][kBins];
+  __shared__ __align__(16) uint32_t share[2][kBins / 2];  // this block's bins, summed over the cluster
+  __shared__ unsigned long long warp_sums[kEvThreads / 32];
+  __shared__ unsigned long long s_shares[kMaxCluster];  // rows of each block's share, both classes
+  __shared__ uint2 s_counts[kMaxCluster];  // each block's rows above and at the threshold
   __shared__ uint32_t s_digit, s_need;
-  __shared__ Counts s_counts;
   const cg::cluster_group cluster = cg::this_cluster();
   const int CS = cluster.num_blocks(), rank = cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -124,216 +122,266 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
   }
   // This block's slots lo .. hi - 1.
   const int chunk = (int)(((int64_t)n + CS * 32 - 1) / (CS * 32)) * 32;
-  const int lo = min(n, rank * chunk), hi = min(n, lo + chunk);
+  const int lo = (int)min((int64_t)n, (int64_t)rank * chunk), hi = min(n, lo + chunk);
   const bool held = chunk <= k.keys;
 
-  // Key and class of the four slots from j on (j a multiple of 4).
-  auto fetch = [&](int j, float (&wv)[4], int32_t (&pv)[4]) {
-    if (j + 4 <= hi) {
-      const float4 x = *reinterpret_cast<const float4*>(w + j);
-      wv[0] = x.x; wv[1] = x.y; wv[2] = x.z; wv[3] = x.w;
-      if (pos) {
-        const int4 y = *reinterpret_cast<const int4*>(pos + j);
-        pv[0] = y.x; pv[1] = y.y; pv[2] = y.z; pv[3] = y.w;
-      }
-    } else {
+  // Weights and positions of the kPerThread slots from j on (j a multiple of it).
+  // The loads of a step are asked for before the step before is worked on; a
+  // block writes only slots that it has read.
+  float wv[kPerThread];
+  int32_t pv[kPerThread];
+  auto fetch = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        wv[i] = j + i < hi ? w[j + i] : 0.f;
-        if (pos) pv[i] = j + i < hi ? pos[j + i] : 0;
+    for (int q = 0; q < kPerThread; q += 4) {
+      if (j + q + 4 <= hi) {
+        const float4 x = *reinterpret_cast<const float4*>(w + j + q);
+        wv[q] = x.x; wv[q + 1] = x.y; wv[q + 2] = x.z; wv[q + 3] = x.w;
+        if (pos) {
+          const int4 y = *reinterpret_cast<const int4*>(pos + j + q);
+          pv[q] = y.x; pv[q + 1] = y.y; pv[q + 2] = y.z; pv[q + 3] = y.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = q; i < q + 4; ++i) {
+          wv[i] = j + i < hi ? w[j + i] : 0.f;
+          pv[i] = pos && j + i < hi ? pos[j + i] : 0;
+        }
       }
     }
     if (!pos) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) pv[i] = j + i;
+      for (int i = 0; i < kPerThread; ++i) pv[i] = j + i;
     }
   };
   uint32_t threshold = 0, need = 0;
   bool active = false;  // the class (protected or not) that the threshold splits
+  uint32_t above = 0, equal = 0;  // rows above and at the threshold before this block's
   if (n > m) {
+    fetch(lo + tid * kPerThread);
     for (int x = 0; x < kHists; ++x)
-      for (int i = tid; i < kBins; i += kEvThreads) hist[x][i] = 0;
+      *reinterpret_cast<uint4*>(&hist[x][4 * tid]) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int base = lo; base < hi; base += kSweep) {
-      const int j = base + tid * 4;
-      float wv[4];
-      int32_t pv[4];
-      uint32_t mine = 0;
-      if (j < hi) {
-        fetch(j, wv, pv);
+      const int j = base + tid * kPerThread;
+      uint32_t key[kPerThread], mine = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t key = weight_key(wv[i]);
-          const bool p = any && pv[i] >= from;
-          mine |= (uint32_t)p << i;
-          if (held) keys[j - lo + i] = key;  // entries behind hi are never read
-          if (j + i < hi) atomicAdd(&hist[p ? 1 : 0][key >> 21], 1u);
-        }
+      for (int i = 0; i < kPerThread; ++i) {
+        key[i] = weight_key(wv[i]);
+        mine |= (uint32_t)(any && pv[i] >= from) << i;
       }
-      if (held && any) {  // eight lanes' bits make a word
-        uint32_t word = mine << (4 * (lane & 7));
+      fetch(j + kSweep);
+      if (j < hi) {
+        if (held) {  // entries behind hi are never counted
+#pragma unroll
+          for (int q = 0; q < kPerThread; q += 4)
+            *reinterpret_cast<uint4*>(keys + j - lo + q) = make_uint4(key[q], key[q + 1], key[q + 2], key[q + 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i)
+          if (j + i < hi) atomicAdd(&hist[(mine >> i) & 1][key[i] >> 21], 1u);
+      }
+      if (held && any) {  // four lanes' bits make a word
+        uint32_t word = mine << (8 * (lane & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, 1);
         word |= __shfl_xor_sync(0xffffffffu, word, 2);
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        if ((lane & 7) == 0 && j < hi) bits[(j - lo) >> 5] = word;
+        if ((lane & 3) == 0 && j < hi) bits[(j - lo) >> 5] = word;
       }
     }
-    cluster.sync();
-    // Digits of 11, 11 and 10 bits; need is the rank left inside the prefix.  A
-    // thread takes two bins, the highest first.
-    uint32_t mask = 0;
+    // Digits of 11, 11 and 10 bits; need is the rank left inside the prefix.
+    // Block r sums the r-th highest share of the bins; a thread takes four.
+    uint32_t mask = 0, mine_above = 0, mine_equal = 0;
+    unsigned long long mine_total;
+    const int bins = kBins / CS;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
       if (pass > 0) {
-        for (int base = lo; base < hi; base += kEvThreads) {
-          const int j = base + tid;
+        for (int base = lo; base < hi; base += kEvThreads * 4) {
+          const int j = base + tid * 4;
           if (j < hi) {
-            const uint32_t key = held ? keys[j - lo] : weight_key(w[j]);
-            const bool p = any && (held ? (bits[(j - lo) >> 5] >> ((j - lo) & 31)) & 1 : (pos ? pos[j] : j) >= from);
-            if (p == active && (key & mask) == threshold) atomicAdd(&hist[pass + 1][(key >> shift) & digits], 1u);
+            uint32_t key[4], prot;
+            const int left = hi - j;
+            if (held) {
+              const uint4 x = *reinterpret_cast<const uint4*>(keys + j - lo);
+              key[0] = x.x; key[1] = x.y; key[2] = x.z; key[3] = x.w;
+              prot = any ? bits[(j - lo) >> 5] >> ((j - lo) & 31) : 0;
+            } else {
+              prot = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                key[i] = j + i < hi ? weight_key(w[j + i]) : 0;
+                prot |= (uint32_t)(any && j + i < hi && (pos ? pos[j + i] : j + i) >= from) << i;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((key[i] & mask) == threshold && i < left && ((prot >> i) & 1) == (uint32_t)active)
+                atomicAdd(&hist[pass + 1][(key[i] >> shift) & digits], 1u);
           }
         }
-        cluster.sync();
       }
-      const int top = kBins - 2 - 2 * tid;
-      uint32_t h1 = 0, h0 = 0, above, total;
-      if (pass == 0 && any) {
-        for (int i = 0; i < CS; ++i) {
-          const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[1][0], i) + top);
-          h0 += v.x;
-          h1 += v.y;
-        }
-        above = scan_excl(h1 + h0, warp_sums, &total);
-        active = total >= (uint32_t)m;
-        need = active ? m : m - total;
-      } else if (pass == 0) {
-        need = m;
-      }
-      if (!(pass == 0 && active)) {
-        h1 = h0 = 0;
-        for (int i = 0; i < CS; ++i) {
-          const uint2 v = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[pass == 0 ? 0 : pass + 1][0], i) + top);
-          h0 += v.x;
-          h1 += v.y;
-        }
-        above = scan_excl(h1 + h0, warp_sums, &total);
-      }
-      if (above < need && need <= above + h1 + h0) {
-        const bool upper = need <= above + h1;
-        s_digit = top + (upper ? 1 : 0);
-        s_need = need - above - (upper ? 0 : h1);
-      }
-      __syncthreads();
-      threshold |= s_digit << shift;
-      mask |= digits << shift;
-      need = s_need;
-      __syncthreads();
-    }
-  }
-  // A row's class in the scan: above the threshold (low half of a word) or at it
-  // (high half); kept are the former and the first `need` of the latter.
-  auto classify = [&](uint32_t key, bool p) -> uint32_t {
-    if (n == m) return 1u;
-    if (p == active) return key > threshold ? 1u : key == threshold ? 0x10000u : 0u;
-    return p ? 1u : 0u;
-  };
-  uint32_t above = 0, equal = 0, below_m = 0;  // before this block's slots; P(m)
-  if (n > m) {
-    Counts c{};
-    for (int base = lo; base < hi; base += kEvThreads) {
-      const int j = base + tid;
-      if (j < hi) {
-        const uint32_t key = held ? keys[j - lo] : weight_key(w[j]);
-        const bool p = any && (held ? (bits[(j - lo) >> 5] >> ((j - lo) & 31)) & 1 : (pos ? pos[j] : j) >= from);
-        const uint32_t cls = classify(key, p);
-        c.above += cls & 0xffff;
-        c.equal += cls >> 16;
-        if (j < m) {
-          c.above_m += cls & 0xffff;
-          c.equal_m += cls >> 16;
+      cluster.sync();
+      const int classes = pass == 0 && any ? 2 : 1;
+      unsigned long long sum = 0, total;
+      if (tid < bins / 4) {
+        const int at = kBins - bins * (rank + 1) + 4 * tid;
+        for (int c = 0; c < classes; ++c) {
+          uint32_t* const h = pass == 0 ? hist[c] : hist[pass + 1];
+          uint4 v[kMaxCluster], all = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i)
+            v[i] = i < CS ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(h, i) + at) : all;
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) {
+            all.x += v[i].x;
+            all.y += v[i].y;
+            all.z += v[i].z;
+            all.w += v[i].w;
+          }
+          if (CS > 1) *reinterpret_cast<uint4*>(&share[c][4 * tid]) = all;
+          sum += (unsigned long long)(all.x + all.y + all.z + all.w) << (32 * c);
         }
       }
-    }
-    if (tid == 0) s_counts = Counts{};
-    __syncthreads();
-    c.above = __reduce_add_sync(0xffffffffu, c.above);
-    c.equal = __reduce_add_sync(0xffffffffu, c.equal);
-    c.above_m = __reduce_add_sync(0xffffffffu, c.above_m);
-    c.equal_m = __reduce_add_sync(0xffffffffu, c.equal_m);
-    if (lane == 0) {
-      atomicAdd(&s_counts.above, c.above);
-      atomicAdd(&s_counts.equal, c.equal);
-      atomicAdd(&s_counts.above_m, c.above_m);
-      atomicAdd(&s_counts.equal_m, c.equal_m);
-    }
-    cluster.sync();
-    uint32_t eq_m = 0;
-    for (int i = 0; i < CS; ++i) {
-      const Counts x = *cluster.map_shared_rank(&s_counts, i);
-      if (i < rank) {
-        above += x.above;
-        equal += x.equal;
+      scan_excl(sum, warp_sums, &total);
+      if (tid < CS) cluster.map_shared_rank(s_shares, tid)[rank] = total;
+      cluster.sync();
+      if (pass == 0) {
+        uint32_t prot = 0;
+        for (int i = 0; i < CS; ++i) prot += (uint32_t)(s_shares[i] >> 32);
+        active = prot >= (uint32_t)m;
+        need = active ? m : m - prot;
       }
-      below_m += x.above_m;
-      eq_m += x.equal_m;
-    }
-    below_m += min(need, eq_m);
-    if (tid == 0 && rank == 0) k.count[bh] = m - (int)below_m;
-  }
-  for (int base = lo; base < hi; base += kSweep) {
-    const int j0 = base + tid * 4;
-    float wv[4];
-    int32_t pv[4];
-    uint32_t cls[4] = {0, 0, 0, 0}, sum = 0;
-    if (j0 < hi) {
-      fetch(j0, wv, pv);
+      // The share that the rank lies in, and the bin in it.
+      const int cls = pass == 0 && active;
+      int owner = 0;
+      for (; owner < CS - 1; ++owner) {
+        const uint32_t rows = (uint32_t)(s_shares[owner] >> (32 * cls));
+        if (need <= rows) break;
+        need -= rows;
+      }
+      const int top = bins - 4 - 4 * tid;  // the highest bins first
+      uint4 v = make_uint4(0, 0, 0, 0);
+      uint32_t* const own = pass == 0 ? hist[cls] : hist[pass + 1];
+      if (top >= 0)
+        v = *reinterpret_cast<const uint4*>(CS > 1 ? cluster.map_shared_rank(share[cls], owner) + top : own + top);
+      uint32_t at = (uint32_t)scan_excl((unsigned long long)(v.x + v.y + v.z + v.w), warp_sums, &total);
+      const uint32_t a[4] = {v.w, v.z, v.y, v.x};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (j0 + i < hi) cls[i] = classify(weight_key(wv[i]), any && pv[i] >= from);
-        sum += cls[i];
+        if (at < need && need <= at + a[i]) {
+          s_digit = kBins - bins * (owner + 1) + top + 3 - i;
+          s_need = need - at;
+        }
+        at += a[i];
       }
-    }
-    uint32_t total;
-    uint32_t run = scan_excl(sum, warp_sums, &total);
+      __syncthreads();
+      const uint32_t digit = s_digit;
+      need = s_need;
+      threshold |= digit << shift;
+      mask |= digits << shift;
+      // This block's own rows above the digit.
+      const uint4 o = *reinterpret_cast<const uint4*>(own + 4 * tid);
+      const uint32_t ov[4] = {o.x, o.y, o.z, o.w};
+      uint32_t more = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = j0 + i;
-      if (j >= hi) continue;
-      const uint32_t eq = equal + (run >> 16);
-      const uint32_t kept_before = above + (run & 0xffff) + min(need, eq);
-      const bool kept = cls[i] == 1u || (cls[i] == 0x10000u && eq < need);
-      if (j < m) {
-        if (kept) {
-          wo[j] = wv[i];
-          if (po) po[j] = pv[i];
-        } else {
-          k.to[bh * k.most + (j - kept_before)] = j;
-        }
-      } else {
-        if (kept) {
-          const int64_t at = bh * k.most + (kept_before - below_m);
-          k.from[at] = j;
-          k.moved_weight[at] = wv[i];
-          if (po) k.moved_position[at] = pv[i];
-        }
-        wo[j] = 0.f;
-        if (po) po[j] = -1;
+      for (int i = 0; i < 4; ++i) more += 4 * tid + i > (int)digit ? ov[i] : 0;
+      if (pass == 0 && any && !active) {  // the protected ones are above all others
+        const uint4 q = *reinterpret_cast<const uint4*>(hist[1] + 4 * tid);
+        more += q.x + q.y + q.z + q.w;
       }
-      run += cls[i];
+      mine_above += more;
+      if (pass == 2) mine_equal = own[digit];
     }
-    above += total & 0xffff;
-    equal += total >> 16;
+    scan_excl((unsigned long long)mine_above, warp_sums, &mine_total);
+    // Told to every block, so that none reads another's memory from here on.
+    if (tid < CS) cluster.map_shared_rank(s_counts, tid)[rank] = make_uint2((uint32_t)mine_total, mine_equal);
+    cluster.sync();
+    for (int i = 0; i < rank; ++i) {
+      above += s_counts[i].x;
+      equal += s_counts[i].y;
+    }
+  }
+  // One scan in slot order over rows above the threshold (low half of a word)
+  // and at it (high half); kept are the former and the first `need` of the
+  // latter.
+  fetch(lo + tid * kPerThread);
+  for (int base = lo; base < hi; base += kSweep) {
+    const int j0 = base + tid * kPerThread;
+    // Bits of the thread's rows that are kept whatever the ties, and of those at
+    // the threshold.
+    uint32_t sure = 0, tied = 0;
+    float x[kPerThread];
+    int32_t y[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      x[i] = wv[i];
+      y[i] = pv[i];
+      const uint32_t key = weight_key(x[i]);
+      const bool p = any && y[i] >= from;
+      const bool split = p == active;
+      sure |= (uint32_t)(split ? key > threshold : p) << i;
+      tied |= (uint32_t)(split && key == threshold) << i;
+    }
+    const uint32_t valid = j0 >= hi ? 0u : (1u << min(kPerThread, hi - j0)) - 1;
+    if (n == m) sure = valid, tied = 0;
+    sure &= valid;
+    tied &= valid;
+    fetch(j0 + kSweep);
+    unsigned long long total;
+    const uint32_t run =
+        (uint32_t)scan_excl((unsigned long long)(__popc(sure) | __popc(tied) << 16), warp_sums, &total);
+    const uint32_t eq = equal + (run >> 16);
+    uint32_t kept = sure;
+    for (uint32_t t = tied, e = eq; t && e < need; t &= t - 1, ++e) kept |= t & -t;
+    const int before = (int)(above + (run & 0xffff) + min(need, eq));  // rows kept below slot j0
+    const uint32_t below = m <= j0 ? 0u : m - j0 >= kPerThread ? valid : (1u << (m - j0)) - 1;  // slots below m
+    if (m >= j0 && m < j0 + kPerThread && m < hi) k.count[bh] = m - (before + __popc(kept & below));
+    for (uint32_t t = valid & below & ~kept; t; t &= t - 1) {
+      const int i = __ffs(t) - 1;
+      k.to[bh * k.most + (j0 + i - before - __popc(kept & ((1u << i) - 1)))] = j0 + i;
+    }
+    if (kept & ~below) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        if ((kept & ~below) >> i & 1) {
+          const int64_t at = bh * k.most + (m - 1 - before - __popc(kept & ((1u << i) - 1)));
+          k.from[at] = j0 + i;
+          k.moved_weight[at] = x[i];
+          if (po) k.moved_position[at] = y[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {  // a given-up slot below m is written by the move
+      x[i] = (below >> i) & 1 ? x[i] : 0.f;
+      y[i] = (below >> i) & 1 ? y[i] : -1;
+    }
+#pragma unroll
+    for (int q = 0; q < kPerThread; q += 4) {
+      if (j0 + q + 4 <= hi) {
+        *reinterpret_cast<float4*>(wo + j0 + q) = make_float4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+        if (po) *reinterpret_cast<int4*>(po + j0 + q) = make_int4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+      } else {
+#pragma unroll
+        for (int i = q; i < q + 4; ++i) {
+          if (j0 + i < hi) {
+            wo[j0 + i] = x[i];
+            if (po) po[j0 + i] = y[i];
+          }
+        }
+      }
+    }
+    above += (uint32_t)total & 0xffff;
+    equal += (uint32_t)total >> 16;
   }
   for (int64_t j = n + rank * kEvThreads + tid; j < k.capacity; j += CS * kEvThreads) {
     wo[j] = 0.f;
     if (po) po[j] = -1;
   }
-  cluster.sync();  // no block leaves while another reads its shared memory
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2)
 evict_move_kernel(const __grid_constant__ EvictCall k) {
   constexpr int L = D / 8;  // lanes of a row
   const int64_t bh = blockIdx.y;
@@ -343,24 +391,52 @@ evict_move_kernel(const __grid_constant__ EvictCall k) {
   const int32_t* table = k.c.table + b * k.c.table_stride;
   const int mask = (1 << k.page_shift) - 1;
   const int lane = threadIdx.x % L;
-  for (int64_t i = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; i < count; i += (int64_t)gridDim.x * (256 / L)) {
-    const int src = k.from[bh * k.most + i], dst = k.to[bh * k.most + i];
-    if (lane == 0) {
-      k.weights_out[bh * k.capacity + dst] = k.moved_weight[bh * k.most + i];
-      if (k.positions_out) k.positions_out[bh * k.capacity + dst] = k.moved_position[bh * k.most + i];
+  constexpr int R = 4;  // rows of a thread in flight
+  const int64_t list = bh * k.most;
+  const int64_t step = (int64_t)gridDim.x * (256 / L);
+  for (int64_t i0 = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; i0 < count; i0 += R * step) {
+    Chunk<T> kc[R], vc[R];
+    int64_t to[R];
+    // Indexes, pages, rows: each kind is asked for R at a time, so that a chain of
+    // three loads serves R rows.
+    int src[R], dst[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const int64_t i = i0 + x * step;
+      src[x] = i < count ? k.from[list + count - 1 - i] : -1;
+      dst[x] = i < count ? k.to[list + i] : 0;
     }
-    const int64_t ps = table[src >> k.page_shift], pd = table[dst >> k.page_shift];
-    if (ps < 0 || ps >= k.c.pages || pd < 0 || pd >= k.c.pages) {
-      if (lane == 0) atomicOr(k.status, kStatusPage);
-      continue;
+    int ps[R], pd[R];
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      ps[x] = src[x] >= 0 ? table[src[x] >> k.page_shift] : -1;
+      pd[x] = src[x] >= 0 ? table[dst[x] >> k.page_shift] : -1;
     }
-    const int64_t as = (((ps * k.c.H + h) << k.page_shift) + (src & mask)) * D + lane * 8;
-    const int64_t ad = (((pd * k.c.H + h) << k.page_shift) + (dst & mask)) * D + lane * 8;
-    Chunk<T> kc, vc;
-    kc.load(static_cast<const T*>(k.c.k) + as);
-    vc.load(static_cast<const T*>(k.c.v) + as);
-    kc.store(static_cast<T*>(k.c.k) + ad);
-    vc.store(static_cast<T*>(k.c.v) + ad);
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      const bool good = ps[x] >= 0 && ps[x] < k.c.pages && pd[x] >= 0 && pd[x] < k.c.pages;
+      to[x] = -1;
+      if (good) {
+        const int64_t as = ((((int64_t)ps[x] * k.c.H + h) << k.page_shift) + (src[x] & mask)) * D + lane * 8;
+        to[x] = ((((int64_t)pd[x] * k.c.H + h) << k.page_shift) + (dst[x] & mask)) * D + lane * 8;
+        kc[x].load(static_cast<const T*>(k.c.k) + as);
+        vc[x].load(static_cast<const T*>(k.c.v) + as);
+      } else if (src[x] >= 0 && lane == 0) {
+        atomicOr(k.status, kStatusPage);
+      }
+    }
+    if (lane < R && i0 + lane * step < count) {  // lane x moves row x's weight and position
+      const int64_t i = i0 + lane * step;
+      const int slot = k.to[list + i];
+      k.weights_out[bh * k.capacity + slot] = k.moved_weight[list + count - 1 - i];
+      if (k.positions_out) k.positions_out[bh * k.capacity + slot] = k.moved_position[list + count - 1 - i];
+    }
+#pragma unroll
+    for (int x = 0; x < R; ++x) {
+      if (to[x] < 0) continue;
+      kc[x].store(static_cast<T*>(k.c.k) + to[x]);
+      vc[x].store(static_cast<T*>(k.c.v) + to[x]);
+    }
   }
 }
 
@@ -402,10 +478,10 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   k.status = device_status_ptr();
   if (!k.status) return cudaErrorInvalidSymbol;
   k.page_shift = __builtin_ctz(c.page);
-  // Blocks of a head: one for each 8192 slots, as long as the GPU has room for
+  // Blocks of a head: one for each 4096 slots, as long as the GPU has room for
   // all of them at once.
   int cs = 1;
-  while (cs < kMaxCluster && k.capacity > (int64_t)cs * 8192 && bh * cs * 2 <= 148 * 2) cs *= 2;
+  while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 148 * 2) cs *= 2;
   const int64_t chunk = (k.capacity + cs * 32 - 1) / (cs * 32) * 32;
   k.keys = chunk <= kMaxKeys ? (int)chunk : 0;
   const size_t smem = (size_t)k.keys * 4 + k.keys / 8;
