@@ -129,65 +129,70 @@ struct QuadCore {
         }
       }
     }
-    for (int t = s.j0 + kw * 8; t < s.j1; t += kParts * 8) {
-      const int j = t + r;
-      bool live = j < s.j1;
-      int64_t page = 0;
-      if (live) {
-        page = k.c.table[s.b * k.c.table_stride + (j >> k.page_shift)];
-        if (page < 0 || page >= k.c.pages) {
-          live = false;
-          if (c4 == 0) atomicOr(k.status, kStatusPage);
-        }
+    // First element of slot j's row, or -1 where there is none.
+    const int32_t* const table = k.c.table + s.b * k.c.table_stride;
+    const int in_page = (1 << k.page_shift) - 1;
+    auto place = [&](int j) -> int64_t {
+      if (j >= s.j1) return -1;
+      const int64_t page = table[j >> k.page_shift];
+      if (page < 0 || page >= k.c.pages) {
+        if (c4 == 0) atomicOr(k.status, kStatusPage);
+        return -1;
       }
-      uint4 kc[NC], vc[NC];
-      const int64_t at = (((page * k.c.H + s.h) << k.page_shift) + (j & ((1 << k.page_shift) - 1))) * D;
+      return (((page * k.c.H + s.h) << k.page_shift) + (j & in_page)) * D + c4 * EPC;
+    };
+    uint4 kc[NC], vc[NC];
+    auto load = [&](uint4 (&c)[NC], const T* p, int64_t at) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        kc[i] = vc[i] = make_uint4(0, 0, 0, 0);
-        if (live) {
-          kc[i] = __ldg(reinterpret_cast<const uint4*>(kp + at) + c4 + 4 * i);
-          vc[i] = __ldg(reinterpret_cast<const uint4*>(vp + at) + c4 + 4 * i);
-        }
+        c[i] = make_uint4(0, 0, 0, 0);
+        if (at >= 0) c[i] = __ldg(reinterpret_cast<const uint4*>(p + at) + 4 * i);
       }
-      float kf[NC * EPC], vf[NC * EPC];
-      const uint32_t* kw_ = reinterpret_cast<const uint32_t*>(kc);
-      const uint32_t* vw_ = reinterpret_cast<const uint32_t*>(vc);
-#pragma unroll
-      for (int i = 0; i < NC * 4; ++i) {
-        if constexpr (sizeof(T) == 2) {
-          kf[2 * i] = __uint_as_float(kw_[i] << 16);
-          kf[2 * i + 1] = __uint_as_float(kw_[i] & 0xffff0000u);
-          vf[2 * i] = __uint_as_float(vw_[i] << 16);
-          vf[2 * i + 1] = __uint_as_float(vw_[i] & 0xffff0000u);
-        } else {
-          kf[i] = __uint_as_float(kw_[i]);
-          vf[i] = __uint_as_float(vw_[i]);
-        }
-      }
+    };
+    auto element = [](const uint4 (&c)[NC], int e) -> float {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(c);
+      if constexpr (sizeof(T) == 2) return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+      else return __uint_as_float(w[e]);
+    };
+    // K of the next tile is asked for as soon as the scores are formed, V as soon
+    // as it is used.
+    int64_t at = place(s.j0 + kw * 8 + r);
+    load(kc, kp, at);
+    load(vc, vp, at);
+    for (int t = s.j0 + kw * 8; t < s.j1; t += kParts * 8) {
+      const int j = t + r;
+      const bool live = at >= 0;
+      const int64_t next = place(j + kParts * 8);
+      float sc[GT];
 #pragma unroll
       for (int i = 0; i < GT; ++i) {
         float x = 0.f;
 #pragma unroll
-        for (int e = 0; e < NC * EPC; ++e) x += q[i][e] * kf[e];
-        x += __shfl_xor_sync(0xffffffffu, x, 1);
-        x += __shfl_xor_sync(0xffffffffu, x, 2);
+        for (int e = 0; e < NC * EPC; ++e) x += q[i][e] * element(kc, e);
+        sc[i] = x;
+      }
+      load(kc, kp, next);
+#pragma unroll
+      for (int i = 0; i < GT; ++i) {
+        sc[i] += __shfl_xor_sync(0xffffffffu, sc[i], 1);
+        sc[i] += __shfl_xor_sync(0xffffffffu, sc[i], 2);
         const int g = hg * GT + i;
         if (k.scores && c4 == 0 && g < s.gn && j < s.j1)
-          k.scores[((int64_t)s.b * k.Hq + s.head0 + g) * capacity + j] = live ? x : -INFINITY;
-        if (!live) continue;
-        if (x > m[i] + kSlack) {  // also the first key: m is -inf
-          const float f = exp2f(m[i] - x);
-          m[i] = x;
+          k.scores[((int64_t)s.b * k.Hq + s.head0 + g) * capacity + j] = live ? sc[i] : -INFINITY;
+        if (sc[i] > m[i] + kSlack && live) {  // also the first key: m is -inf
+          const float f = exp2f(m[i] - sc[i]);
+          m[i] = sc[i];
           l[i] *= f;
 #pragma unroll
           for (int e = 0; e < NC * EPC; ++e) o[i][e] *= f;
         }
-        const float p = exp2f(x - m[i]);
+        const float p = live ? exp2f(sc[i] - m[i]) : 0.f;
         l[i] += p;
 #pragma unroll
-        for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * vf[e];
+        for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * element(vc, e);
       }
+      load(vc, vp, next);
+      at = next;
     }
     // Join the eight key rows of the warp.
 #pragma unroll
