@@ -455,6 +455,14 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
   const int Hv = k.c.H * k.nv;
   cudaTriggerProgrammaticLaunchCompletion();
 
+  for (int b = blockIdx.x; b < k.c.B; b += gridDim.x) {
+    const int len = k.c.lengths[b];
+    if (tid == 0 && (len < 0 || len > k.c.width << k.page_shift)) atomicOr(k.status, kStatusPage);
+    if (len > 0) continue;
+    for (int64_t i = tid; i < (int64_t)k.Hq * D; i += kDecThreads)
+      static_cast<T*>(k.o)[(int64_t)b * k.Hq * D + i] = (T)0.f;
+    for (int i = tid; i < k.Hq; i += kDecThreads) k.lse[(int64_t)b * k.Hq + i] = -INFINITY;
+  }
   int64_t sum = 0;
   for (int b = tid; b < k.c.B; b += kDecThreads) sum += tiles_of(seq_length(k, b));
   const int64_t T_all = block_sum<kDecThreads>(sum, warp_sums) * Hv;
@@ -547,14 +555,15 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
 // Joins the parts of one query head (blockIdx.y = 0 writes O and lse) and adds
 // the probabilities of kJoinSlots slots to the weights of its key head.
 // Without weights the grid is (B * Hq); with them (B * H, slot blocks) and the
-// block goes over the group's heads.  Launched while decode_kernel still runs:
+// block goes over the group's heads.  NT threads: each warp takes every NT/32-th
+// part, so that a few heads with many parts wait for one load latency, not four.  Launched while decode_kernel still runs:
 // what it needs of lengths and ranges is worked out before the wait.
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
-join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
-  constexpr int NW = kJoinThreads / 32, E = D / 32;
+template <typename T, int D, int NT, bool with_weights>
+__global__ void __launch_bounds__(NT)
+join_kernel(const __grid_constant__ DecodeCall k) {
+  constexpr int NW = NT / 32, E = D / 32, kClasses = 16, kPer = kClasses / NW;
   __shared__ int64_t warp_sums[NW];
-  __shared__ float s_f[kMaxBlocks], s_red[NW], s_acc[NW][D];
+  __shared__ float s_f[kMaxBlocks], s_red[4], s_acc[kClasses][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per_b = with_weights ? k.c.H : k.Hq;
   const int b = blockIdx.x / per_b;
@@ -562,25 +571,21 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
   const int heads = with_weights ? k.G : 1;
   const int n = seq_length(k, b);
   const int slot0 = blockIdx.y * kJoinSlots;
-  if (blockIdx.y > 0 && slot0 >= n) return;
+  if (slot0 >= n) return;  // also an empty sequence: decode_kernel has answered it
   const int Hv = k.c.H * k.nv;
   const int64_t capacity = (int64_t)k.c.width << k.page_shift;
 
   int64_t all = 0, before = 0;
-  for (int i = tid; i < k.c.B; i += kJoinThreads) {
+  for (int i = tid; i < k.c.B; i += NT) {
     const int64_t t = tiles_of(seq_length(k, i));
     all += t;
     if (i < b) before += t;
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
-      const int len = k.c.lengths[i];
-      if (len < 0 || len > capacity) atomicOr(k.status, kStatusPage);
-    }
   }
-  const int64_t T_all = block_sum<kJoinThreads>(all, warp_sums) * Hv;
-  const int64_t first = block_sum<kJoinThreads>(before, warp_sums) * Hv;
+  const int64_t T_all = block_sum<NT>(all, warp_sums) * Hv;
+  const int64_t first = block_sum<NT>(before, warp_sums) * Hv;
   const int nt = tiles_of(n);
   const int W = ranges(k, T_all);
-  static_assert(kJoinSlots == 4 * kJoinThreads, "four slots a thread");
+  static_assert(!with_weights || kJoinSlots == 4 * NT, "four slots a thread");
   const int j0 = slot0 + tid * 4;
   float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
   if (with_weights && j0 < n)
@@ -590,11 +595,6 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
   for (int i = 0; i < heads; ++i) {
     const int head = head_first + i;
     const int64_t row = (int64_t)b * k.Hq + head;
-    if (n == 0) {
-      for (int e = tid; e < D; e += kJoinThreads) static_cast<T*>(k.o)[row * D + e] = (T)0.f;
-      if (tid == 0) k.lse[row] = -INFINITY;
-      continue;
-    }
     const int g = head % k.G;
     const int hv = head / k.G * k.nv + g / k.gv;
     const int64_t seg0 = first + (int64_t)hv * nt, seg1 = seg0 + nt;
@@ -610,50 +610,61 @@ join_kernel(const __grid_constant__ DecodeCall k, bool with_weights) {
       const float* base = k.part + (int64_t)c0 * 2 * stride + (int64_t)(g % k.gv) * (D + 4);
       const int parts = c1 - c0 + 1;
       auto part = [&](int c) { return base + (2 * (int64_t)c + (c == 0 ? late : 0)) * stride; };
+      // The order of the sums is that of 128 threads and 16 classes of parts
+      // whatever NT is, so the form of the launch does not show in the bits.
       float top = -INFINITY;
-      for (int c = tid; c < parts; c += kJoinThreads) {
-        s_f[c] = part(c)[D];
-        top = fmaxf(top, s_f[c]);
-      }
-#pragma unroll
-      for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      if (lane == 0) s_red[warp] = top;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, s_red[w]);
-      __syncthreads();
-      float tot = 0.f;
-      for (int c = tid; c < parts; c += kJoinThreads) {
-        const float f = s_f[c] == -INFINITY ? 0.f : exp2f(s_f[c] - top);
-        s_f[c] = f;
-        tot += f * part(c)[D + 1];
-      }
-#pragma unroll
-      for (int x = 16; x; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
-      if (lane == 0) s_red[warp] = tot;
-      __syncthreads();
-      tot = 0.f;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) tot += s_red[w];
-      lse2 = top + log2f(tot);
-      if (blockIdx.y == 0) {
-        float acc[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-        for (int c = warp; c < parts; c += NW) {
-          const float f = s_f[c];
-          const float* p = part(c);
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += f * p[lane + 32 * e];
+      if (tid < 128) {
+        for (int c = tid; c < parts; c += 128) {
+          s_f[c] = part(c)[D];
+          top = fmaxf(top, s_f[c]);
         }
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_acc[warp][lane + 32 * e] = acc[e];
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        if (lane == 0) s_red[warp] = top;
+      }
+      __syncthreads();
+      top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+      __syncthreads();
+      float tot = 0.f;
+      if (tid < 128) {
+        for (int c = tid; c < parts; c += 128) {
+          const float f = s_f[c] == -INFINITY ? 0.f : exp2f(s_f[c] - top);
+          s_f[c] = f;
+          tot += f * part(c)[D + 1];
+        }
+#pragma unroll
+        for (int x = 16; x; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
+        if (lane == 0) s_red[warp] = tot;
+      }
+      __syncthreads();
+      tot = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
+      lse2 = top + log2f(tot);
+      if (blockIdx.y == 0) {
+        float acc[kPer][E];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+        for (int c = 0; c < parts; c += kClasses) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int x = c + warp + NW * i;
+            if (x >= parts) continue;
+            const float f = s_f[x];
+            const float* p = part(x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[i][e] += f * p[lane + 32 * e];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+          for (int e = 0; e < E; ++e) s_acc[warp + NW * i][lane + 32 * e] = acc[i][e];
         __syncthreads();
-        for (int e = tid; e < D; e += kJoinThreads) {
+        for (int e = tid; e < D; e += NT) {
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < NW; ++w) v += s_acc[w][e];
+          for (int w = 0; w < kClasses; ++w) v += s_acc[w][e];
           static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? v / tot : 0.f);
         }
         if (tid == 0) k.lse[row] = tot > 0.f ? lse2 * kLn2 : -INFINITY;
@@ -762,18 +773,23 @@ cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void
   with_core(c.dtype, c.d, k.gv, [&]<typename Core>() {
     decode_kernel<Core><<<k.blocks, kDecThreads, 0, st>>>(k);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return;
     const int64_t capacity = (int64_t)c.width * c.page;
+    if (e != cudaSuccess || (capacity <= kTile && !ww)) return;  // one tile a head: no range splits it
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ww ? c.B * c.H : c.B * Q.H, ww ? (unsigned)((capacity + kJoinSlots - 1) / kJoinSlots) : 1);
-    cfg.blockDim = dim3(kJoinThreads);
+    // One block an SM at most: many warps, for the parts are many; else few.
+    const bool few = !ww && cfg.gridDim.x <= 148;
+    cfg.blockDim = dim3(few ? 512 : kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute overlap{};
     overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     overlap.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &overlap;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, join_kernel<typename Core::T, Core::D>, k, ww);
+    using T = typename Core::T;
+    constexpr int D = Core::D;
+    e = cudaLaunchKernelEx(&cfg, ww ? join_kernel<T, D, kJoinThreads, true>
+                                 : few ? join_kernel<T, D, 512, false> : join_kernel<T, D, kJoinThreads, false>, k);
   });
   return e != cudaSuccess ? e : cudaGetLastError();
 }
