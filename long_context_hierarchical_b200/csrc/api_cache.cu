@@ -123,9 +123,11 @@ lh_status check_cache(const lh_cache* c, bool pointers = true) {
   return LH_OK;
 }
 
-lh_status check_heads(const lh_cache* c, int64_t Hq) {
+lh_status check_heads(const lh_cache* c, int64_t Hq, bool with_weights) {
   if (Hq < 1 || Hq % c->H != 0) return fail(LH_ERR_INVALID_ARG, "Hq must be a multiple of the cache's H");
   if ((int64_t)c->B * Hq > (int64_t(1) << 22)) return fail(LH_ERR_UNSUPPORTED, "B * Hq above 2^22 is not built");
+  if (!decode_fits(*c, Hq, with_weights))
+    return fail(LH_ERR_UNSUPPORTED, "weights of more than about 2^40 slots are not built");
   return LH_OK;
 }
 
@@ -248,7 +250,7 @@ lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, i
 }
 
 int64_t lh_decode_ws_bytes(const lh_cache* cache, int64_t Hq, int32_t with_weights) {
-  if (check_cache(cache, false) != LH_OK || check_heads(cache, Hq) != LH_OK) return -1;
+  if (check_cache(cache, false) != LH_OK || check_heads(cache, Hq, with_weights != 0) != LH_OK) return -1;
   return decode_ws_bytes(*cache, Hq, with_weights != 0);
 }
 
@@ -258,7 +260,7 @@ lh_status lh_decode(const lh_cache* cache, const lh_rows* Q, float scale, void* 
   Range range("lh_decode");
   LH_TRY(check_cache(cache));
   LH_TRY(check_rows(Q, "Q", cache->B, 1, cache->dtype, false, cache->d));
-  LH_TRY(check_heads(cache, Q->H));
+  LH_TRY(check_heads(cache, Q->H, weights != nullptr));
   if (!isfinite(scale)) return fail(LH_ERR_INVALID_ARG, "scale must be finite");
   LH_CHECK_PTR(O);
   LH_CHECK_INDEX(lse);

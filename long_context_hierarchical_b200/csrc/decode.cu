@@ -52,6 +52,7 @@ struct DecodeCall {
   int page_shift, Hq, G;  // G = Hq / H
   int nv, gv;         // parts of a key head's group, query heads of a part
   int blocks;         // ranges of the split
+  int slot_blocks;    // join blocks of a key head's slots
 };
 
 __device__ __forceinline__ int seq_length(const DecodeCall& k, int b) {
@@ -552,28 +553,69 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
   }
 }
 
-// Joins the parts of one query head (blockIdx.y = 0 writes O and lse) and adds
-// the probabilities of kJoinSlots slots to the weights of its key head.
-// Without weights the grid is (B * Hq); with them (B * H, slot blocks) and the
-// block goes over the group's heads.  NT threads: each warp takes every NT/32-th
-// part, so that a few heads with many parts wait for one load latency, not four.  Launched while decode_kernel still runs:
-// what it needs of lengths and ranges is worked out before the wait.
+// Where the parts of a query head are: part c is the row of `of(c)`, c < count;
+// none (count 0) where one range held the whole sequence and wrote its answer.
+template <int D>
+struct Parts {
+  const float* base;
+  int64_t stride;
+  int count, late;
+  __device__ __forceinline__ const float* of(int c) const {
+    return base + (2 * (int64_t)c + (c == 0 ? late : 0)) * stride;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ Parts<D> parts_of(const DecodeCall& k, int head, int64_t first, int nt, int64_t T_all, int W) {
+  const int g = head % k.G;
+  const int hv = head / k.G * k.nv + g / k.gv;
+  const int64_t seg0 = first + (int64_t)hv * nt, seg1 = seg0 + nt;
+  const int c0 = range_of(seg0, T_all, W), c1 = range_of(seg1 - 1, T_all, W);
+  Parts<D> p;
+  p.stride = (int64_t)k.gv * (D + 4);
+  p.base = k.part + (int64_t)c0 * 2 * p.stride + (int64_t)(g % k.gv) * (D + 4);
+  p.late = range_begin(c0, T_all, W) < seg0;  // range c0 holds another segment before: slot 1
+  p.count = c0 == c1 ? 0 : c1 - c0 + 1;
+  return p;
+}
+
+// Adds (m, l) to a running pair; returns the factors of the two sides.
+__device__ __forceinline__ float2 merge(float& m, float& l, float m2, float l2) {
+  const float top = fmaxf(m, m2);
+  const float2 f = make_float2(m == -INFINITY ? 0.f : exp2f(m - top), m2 == -INFINITY ? 0.f : exp2f(m2 - top));
+  m = top;
+  l = l * f.x + l2 * f.y;
+  return f;
+}
+
+// Joins the parts of a query head and, with weights, adds the probabilities to
+// the slots of a key head.  A block of the first kind answers one head: its
+// parts fall in 16 classes, a warp's of one class in turn, so that one load
+// latency serves them all, and the classes are joined in their order; NT threads
+// do not show in the bits.  A block of the second kind works out the lse of its
+// key head's queries, a warp each, and adds kJoinSlots slots.  Grid: per
+// (sequence, key head), G blocks of the first kind, then those of the second.
+// Launched while decode_kernel still runs: what it needs of lengths and ranges is
+// worked out before the wait.  Every block waits, those without work too: the next
+// launch of the stream waits for this one alone, and must find decode_kernel done.
 template <typename T, int D, int NT, bool with_weights>
 __global__ void __launch_bounds__(NT)
 join_kernel(const __grid_constant__ DecodeCall k) {
-  constexpr int NW = NT / 32, E = D / 32, kClasses = 16, kPer = kClasses / NW;
+  constexpr int NW = NT / 32, E = D / 32, kClasses = 16, kPer = kClasses / NW, kChunk = 32;
   __shared__ int64_t warp_sums[NW];
-  __shared__ float s_f[kMaxBlocks], s_red[4], s_acc[kClasses][D];
+  __shared__ float s_m[kClasses], s_l[kClasses], s_acc[kClasses][D], s_lse[kChunk];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int per_b = with_weights ? k.c.H : k.Hq;
-  const int b = blockIdx.x / per_b;
-  const int head_first = with_weights ? (blockIdx.x % per_b) * k.G : blockIdx.x % per_b;
-  const int heads = with_weights ? k.G : 1;
-  const int n = seq_length(k, b);
-  const int slot0 = blockIdx.y * kJoinSlots;
-  if (slot0 >= n) return;  // also an empty sequence: decode_kernel has answered it
-  const int Hv = k.c.H * k.nv;
   const int64_t capacity = (int64_t)k.c.width << k.page_shift;
+  const int per = k.G + (with_weights ? k.slot_blocks : 0);
+  const int64_t bh = blockIdx.x / per;
+  const int kind = (int)(blockIdx.x - bh * per);
+  const int b = (int)(bh / k.c.H), h = (int)(bh % k.c.H);
+  const int n = seq_length(k, b);
+  const int slot0 = (kind - k.G) * kJoinSlots;
+  if (n == 0 || slot0 >= n) {  // decode_kernel has answered an empty sequence
+    cudaGridDependencySynchronize();
+    return;
+  }
 
   int64_t all = 0, before = 0;
   for (int i = tid; i < k.c.B; i += NT) {
@@ -581,107 +623,111 @@ join_kernel(const __grid_constant__ DecodeCall k) {
     all += t;
     if (i < b) before += t;
   }
+  const int Hv = k.c.H * k.nv;
   const int64_t T_all = block_sum<NT>(all, warp_sums) * Hv;
   const int64_t first = block_sum<NT>(before, warp_sums) * Hv;
   const int nt = tiles_of(n);
   const int W = ranges(k, T_all);
+
+  if (kind < k.G) {
+    const int head = h * k.G + kind;
+    const int64_t row = (int64_t)b * k.Hq + head;
+    const Parts<D> parts = parts_of<D>(k, head, first, nt, T_all, W);
+    cudaGridDependencySynchronize();
+    if (parts.count == 0) return;
+    float acc[kPer][E], m[kPer], l[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
+    }
+#pragma unroll 2
+    for (int c = 0; c < parts.count; c += kClasses) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int x = c + warp + NW * i;
+        if (x >= parts.count) continue;
+        const float* p = parts.of(x);
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = p[lane + 32 * e];
+        const float2 f = merge(m[i], l[i], p[D], p[D + 1]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[i][e] = acc[i][e] * f.x + v[e] * f.y;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_acc[warp + NW * i][lane + 32 * e] = acc[i][e];
+      if (lane == 0) {
+        s_m[warp + NW * i] = m[i];
+        s_l[warp + NW * i] = l[i];
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < D; e += NT) {
+      float top = -INFINITY, tot = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kClasses; ++w) top = fmaxf(top, s_m[w]);
+#pragma unroll
+      for (int w = 0; w < kClasses; ++w) {
+        const float f = s_m[w] == -INFINITY ? 0.f : exp2f(s_m[w] - top);
+        tot += f * s_l[w];
+        v += f * s_acc[w][e];
+      }
+      static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? v / tot : 0.f);
+      if (e == 0) k.lse[row] = tot > 0.f ? (top + log2f(tot)) * kLn2 : -INFINITY;
+    }
+    return;
+  }
+
   static_assert(!with_weights || kJoinSlots == 4 * NT, "four slots a thread");
   const int j0 = slot0 + tid * 4;
+  const int64_t slots = bh * capacity;
   float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (with_weights && j0 < n)
-    add = *reinterpret_cast<const float4*>(k.weights + ((int64_t)b * k.c.H + head_first / k.G) * capacity + j0);
+  if (j0 < n) add = *reinterpret_cast<const float4*>(k.weights + slots + j0);
   cudaGridDependencySynchronize();
-
-  for (int i = 0; i < heads; ++i) {
-    const int head = head_first + i;
-    const int64_t row = (int64_t)b * k.Hq + head;
-    const int g = head % k.G;
-    const int hv = head / k.G * k.nv + g / k.gv;
-    const int64_t seg0 = first + (int64_t)hv * nt, seg1 = seg0 + nt;
-    const int c0 = range_of(seg0, T_all, W), c1 = range_of(seg1 - 1, T_all, W);
-    float lse2;
-    if (c0 == c1) {
-      lse2 = k.lse[row] * kLog2e;
-    } else {
-      // Part c - c0: slot 0 of range c, or slot 1 of range c0 where that holds
-      // another segment before.
-      const int64_t stride = (int64_t)k.gv * (D + 4);
-      const int late = range_begin(c0, T_all, W) < seg0;
-      const float* base = k.part + (int64_t)c0 * 2 * stride + (int64_t)(g % k.gv) * (D + 4);
-      const int parts = c1 - c0 + 1;
-      auto part = [&](int c) { return base + (2 * (int64_t)c + (c == 0 ? late : 0)) * stride; };
-      // The order of the sums is that of 128 threads and 16 classes of parts
-      // whatever NT is, so the form of the launch does not show in the bits.
-      float top = -INFINITY;
-      if (tid < 128) {
-        for (int c = tid; c < parts; c += 128) {
-          s_f[c] = part(c)[D];
-          top = fmaxf(top, s_f[c]);
+  for (int h0 = 0; h0 < k.G; h0 += kChunk) {
+    const int heads = min(kChunk, k.G - h0);
+    __syncthreads();
+    for (int i = warp; i < heads; i += NW) {
+      const int head = h * k.G + h0 + i;
+      const Parts<D> parts = parts_of<D>(k, head, first, nt, T_all, W);
+      float lse2;
+      if (parts.count == 0) {
+        lse2 = k.lse[(int64_t)b * k.Hq + head] * kLog2e;
+      } else {
+        float m = -INFINITY, l = 0.f;
+        for (int c = lane; c < parts.count; c += 32) {
+          const float* p = parts.of(c);
+          merge(m, l, p[D], p[D + 1]);
         }
 #pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        if (lane == 0) s_red[warp] = top;
+        for (int x = 16; x; x >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m, x), l2 = __shfl_xor_sync(0xffffffffu, l, x);
+          merge(m, l, m2, l2);
+        }
+        lse2 = m + log2f(l);
       }
-      __syncthreads();
-      top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-      __syncthreads();
-      float tot = 0.f;
-      if (tid < 128) {
-        for (int c = tid; c < parts; c += 128) {
-          const float f = s_f[c] == -INFINITY ? 0.f : exp2f(s_f[c] - top);
-          s_f[c] = f;
-          tot += f * part(c)[D + 1];
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, x);
-        if (lane == 0) s_red[warp] = tot;
-      }
-      __syncthreads();
-      tot = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-      lse2 = top + log2f(tot);
-      if (blockIdx.y == 0) {
-        float acc[kPer][E];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
-        for (int c = 0; c < parts; c += kClasses) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int x = c + warp + NW * i;
-            if (x >= parts) continue;
-            const float f = s_f[x];
-            const float* p = part(x);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[i][e] += f * p[lane + 32 * e];
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-#pragma unroll
-          for (int e = 0; e < E; ++e) s_acc[warp + NW * i][lane + 32 * e] = acc[i][e];
-        __syncthreads();
-        for (int e = tid; e < D; e += NT) {
-          float v = 0.f;
-#pragma unroll
-          for (int w = 0; w < kClasses; ++w) v += s_acc[w][e];
-          static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? v / tot : 0.f);
-        }
-        if (tid == 0) k.lse[row] = tot > 0.f ? lse2 * kLn2 : -INFINITY;
-      }
-      __syncthreads();
+      if (lane == 0) s_lse[i] = lse2;
     }
-    if (with_weights && j0 < n) {
+    __syncthreads();
+    if (j0 >= n) continue;
+    for (int i = 0; i < heads; ++i) {
       // Slots from n on hold nothing: their sums are not stored.
-      const float4 s = *reinterpret_cast<const float4*>(k.scores + row * capacity + j0);
-      add.x += s.x == -INFINITY ? 0.f : exp2f(s.x - lse2);
-      add.y += s.y == -INFINITY ? 0.f : exp2f(s.y - lse2);
-      add.z += s.z == -INFINITY ? 0.f : exp2f(s.z - lse2);
-      add.w += s.w == -INFINITY ? 0.f : exp2f(s.w - lse2);
+      const float4 s = *reinterpret_cast<const float4*>(
+          k.scores + ((int64_t)b * k.Hq + h * k.G + h0 + i) * capacity + j0);
+      add.x += s.x == -INFINITY ? 0.f : exp2f(s.x - s_lse[i]);
+      add.y += s.y == -INFINITY ? 0.f : exp2f(s.y - s_lse[i]);
+      add.z += s.z == -INFINITY ? 0.f : exp2f(s.z - s_lse[i]);
+      add.w += s.w == -INFINITY ? 0.f : exp2f(s.w - s_lse[i]);
     }
   }
-  if (with_weights && j0 < n) {
-    float* out = k.weights_out + ((int64_t)b * k.c.H + head_first / k.G) * capacity + j0;
+  if (j0 < n) {
+    float* out = k.weights_out + slots + j0;
     if (j0 + 4 <= n) {
       *reinterpret_cast<float4*>(out) = add;
     } else {
@@ -742,6 +788,11 @@ Sizes sizes(const lh_cache& c, int64_t Hq, bool with_weights) {
 
 }  // namespace
 
+bool decode_fits(const lh_cache& c, int64_t Hq, bool with_weights) {
+  const int64_t slots = with_weights ? ((int64_t)c.width * c.page + kJoinSlots - 1) / kJoinSlots : 0;
+  return (int64_t)c.B * c.H * (Hq / c.H + slots) < (int64_t(1) << 31);
+}
+
 int64_t decode_ws_bytes(const lh_cache& c, int64_t Hq, bool with_weights) {
   const Sizes s = sizes(c, Hq, with_weights);
   return s.part + s.scores;
@@ -769,6 +820,7 @@ cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void
   k.nv = z.nv;
   k.gv = z.gv;
   k.blocks = z.blocks;
+  k.slot_blocks = (int)(((int64_t)c.width * c.page + kJoinSlots - 1) / kJoinSlots);
   cudaError_t e = cudaSuccess;
   with_core(c.dtype, c.d, k.gv, [&]<typename Core>() {
     decode_kernel<Core><<<k.blocks, kDecThreads, 0, st>>>(k);
@@ -776,7 +828,7 @@ cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void
     const int64_t capacity = (int64_t)c.width * c.page;
     if (e != cudaSuccess || (capacity <= kTile && !ww)) return;  // one tile a head: no range splits it
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ww ? c.B * c.H : c.B * Q.H, ww ? (unsigned)((capacity + kJoinSlots - 1) / kJoinSlots) : 1);
+    cfg.gridDim = dim3((unsigned)((int64_t)c.B * c.H * (k.G + (ww ? k.slot_blocks : 0))));
     // One block an SM at most: many warps, for the parts are many; else few.
     const bool few = !ww && cfg.gridDim.x <= 148;
     cfg.blockDim = dim3(few ? 512 : kJoinThreads);

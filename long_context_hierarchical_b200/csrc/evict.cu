@@ -377,30 +377,50 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
       }
       const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
       sum -= both;
-      uint32_t ab = above + (sum & 0xffff), eq = equal + (sum >> 16);
+      const uint32_t eq = equal + (sum >> 16);
+      const int kept_before = (int)(above + (sum & 0xffff) + min(need, eq));
       above += all & 0xffff;
       equal += all >> 16;
-      if (j < whi) {
+      uint32_t kept = a;
+      if (__any_sync(0xffffffffu, e != 0)) {  // rare: rows at the threshold
+        uint32_t x = eq;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int kept_before = (int)(ab + min(need, eq));
-          const bool kept = (a >> i & 1) || ((e >> i & 1) && eq < need);
-          ab += a >> i & 1;
-          eq += e >> i & 1;
-          const bool low = j + i < m;
-          if (j + i == m && m < whi) k.count[bh] = m - kept_before;
-          if (low != kept && j + i < whi) {
-            if (low) {
-              to[j + i - kept_before] = j + i;  // its weight is written by the move
-            } else {
-              const int at = m - 1 - kept_before;
+          if (e >> i & 1) {
+            if (x < need) kept |= 1u << i;
+            ++x;
+          }
+        }
+      }
+      if (j < whi) {
+        const uint32_t valid = (1u << min(4, whi - j)) - 1;
+        const uint32_t low = j + 4 <= m ? 15u : j >= m ? 0u : (1u << (m - j)) - 1;  // slots below m
+        if (m >= j && m < j + 4 && m < whi) k.count[bh] = m - kept_before - __popc(kept & low);
+        const uint32_t holes = ~kept & low & valid;  // their weights are written by the move
+        if (holes) {
+          int32_t* const p = to + (j - kept_before);
+          if (holes & 1) p[0] = j;
+          if (holes & 2) p[holes & 1] = j + 1;
+          if (holes & 4) p[__popc(holes & 3)] = j + 2;
+          if (holes & 8) p[__popc(holes & 7)] = j + 3;
+        }
+        const uint32_t moving = kept & ~low;
+        if (moving) {
+          const int last = m - 1 - kept_before - __popc(kept & low);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (moving >> i & 1) {
+              const int at = last - __popc(moving & ((1u << i) - 1));
               src[at] = j + i;
               mw[at] = x[r][i];
               if (POS) mp[at] = y[r][i];
             }
           }
-          x[r][i] = low ? x[r][i] : 0.f;
-          y[r][i] = low ? y[r][i] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[r][i] = (low >> i & 1) ? x[r][i] : 0.f;
+          y[r][i] = (low >> i & 1) ? y[r][i] : -1;
         }
         if (j + 4 <= whi) {
           *reinterpret_cast<float4*>(wo + j) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
@@ -501,10 +521,12 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   k.status = device_status_ptr();
   if (!k.status) return cudaErrorInvalidSymbol;
   k.page_shift = __builtin_ctz(c.page);
-  // Blocks of a head: one for each 4096 slots, as long as the GPU has room for
-  // all of them at once.
+  // Blocks of a head: one for each 4096 slots, as long as every block has an SM of
+  // its own (15 clusters of eight fit side by side, 33 of four; at 16 heads of
+  // 98K slots eight blocks a head put two on some SMs, and those took 35 us where the others
+  // took 24).
   int cs = 1;
-  while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 148 * 2) cs *= 2;
+  while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 120) cs *= 2;
   const int64_t chunk = (k.capacity + cs * 128 - 1) / (cs * 128) * 128;
   k.keys = chunk <= kMaxKeys ? (int)chunk : 0;
   const size_t smem = (size_t)k.keys * 4 + k.keys / 4;

@@ -100,6 +100,8 @@ cudaError_t launch_cache_append(const lh_cache& c, const lh_rotary_plan* rotary,
                                 const RowsArg& K, const RowsArg& V, const RowsArg& Q, const RowsArg& Qo,
                                 const int32_t* positions, int64_t positions_stride,
                                 const int32_t* counts, int32_t* slot_positions, cudaStream_t st);
+// Whether the call's join fits one launch.
+bool decode_fits(const lh_cache& c, int64_t Hq, bool with_weights);
 int64_t decode_ws_bytes(const lh_cache& c, int64_t Hq, bool with_weights);
 cudaError_t launch_decode(const lh_cache& c, const RowsArg& Q, float scale, void* O, float* lse,
                           const float* weights, float* weights_out, void* ws, cudaStream_t st);
