@@ -315,7 +315,7 @@ typedef struct {
 /* Turn `count` tensors (1 or 2: Q, or Q and K; their H may differ) of B
  * sequences of N rows: Y[i] from X[i].  Row n of sequence b stands at
  * positions[b * positions_stride + n], or at start + n where positions is
- * NULL.  transpose != 0 applies the transposed map, which is the gradient of
+ * NULL (within 32 bits, like them).  transpose != 0 applies the transposed map, which is the gradient of
  * the plain one.  Y[i] may be X[i] itself (same pointer and strides);
  * otherwise none of the Y may overlap another tensor of the call.  Inputs may
  * repeat rows by zero strides, outputs may not.  fp32 arithmetic, rounded
@@ -336,8 +336,8 @@ lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_
  * their contents.  A length outside 0 .. capacity is clamped, a row whose
  * page index is outside 0 .. pages - 1 is left out (not written, not
  * attended to), and either sets the device status word to LH_ERR_PAGE.
- * Built here: d in {64, 128}, page a power of two, 16 to 65536, capacity below
- * 2^31 - 2^16.  Index arrays (table, lengths, counts, positions, protect) need
+ * Built here: d in {64, 128}, page a power of two, 16 to 65536, capacity at most
+ * 2^31 - 2^16, B * H at most 65535.  k and v must not overlap.  Index arrays (table, lengths, counts, positions, protect) need
  * 4-byte alignment only. */
 typedef struct {
   void *k, *v;            /* [pages, H, page, d] */
@@ -372,7 +372,8 @@ lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, i
  * [B, Hq] fp32.  weights and weights_out ([B, H, capacity] fp32, both or
  * neither, possibly the same array): for every slot j < lengths[b]
  *   weights_out[b,h,j] = weights[b,h,j] + sum over head h's queries exp(s_j - lse);
- * the entries behind are not touched.  ws: lh_decode_ws_bytes() bytes, contents
+ * the entries behind are not touched.  A NaN among q, k and v makes the outputs that
+ * it enters NaN; what lies behind a length is never read.  ws: lh_decode_ws_bytes() bytes, contents
  * on entry ignored; calls that overlap on the GPU (two streams, two graphs)
  * need one each.  Results do not depend on scheduling. */
 int64_t lh_decode_ws_bytes(const lh_cache* cache, int64_t Hq, int32_t with_weights);

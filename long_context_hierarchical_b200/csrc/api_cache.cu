@@ -96,6 +96,12 @@ lh_status check_pair(const lh_rows& x, const lh_rows& y, const char* name, int64
   return LH_OK;
 }
 
+// An in-place array: the output is the input itself or lies apart from it.
+bool same_or_apart(const void* in, const void* out, int64_t bytes) {
+  const char *a = static_cast<const char*>(in), *c = static_cast<const char*>(out);
+  return a == c || a + bytes <= c || c + bytes <= a;
+}
+
 RowsArg rows_arg(const lh_rows* x) {
   if (!x) return RowsArg{};
   return RowsArg{x->ptr, x->stride_b, x->stride_h, x->stride_n, (int)x->H};
@@ -120,6 +126,8 @@ lh_status check_cache(const lh_cache* c, bool pointers = true) {
   const void *k = c->k, *v = c->v, *table = c->table, *lengths = c->lengths;
   LH_CHECK_PTR(k); LH_CHECK_PTR(v);
   LH_CHECK_INDEX(table); LH_CHECK_INDEX(lengths);
+  const int64_t bytes = c->pages * c->H * c->page * c->d * (c->dtype == LH_BF16 ? 2 : 4);
+  if (k == v || !same_or_apart(k, v, bytes)) return fail(LH_ERR_INVALID_ARG, "k and v overlap");
   return LH_OK;
 }
 
@@ -129,12 +137,6 @@ lh_status check_heads(const lh_cache* c, int64_t Hq, bool with_weights) {
   if (!decode_fits(*c, Hq, with_weights))
     return fail(LH_ERR_UNSUPPORTED, "weights of more than about 2^40 slots are not built");
   return LH_OK;
-}
-
-// An in-place array: the output is the input itself or lies apart from it.
-bool same_or_apart(const void* in, const void* out, int64_t bytes) {
-  const char *a = static_cast<const char*>(in), *c = static_cast<const char*>(out);
-  return a == c || a + bytes <= c || c + bytes <= a;
 }
 
 int64_t slots_bytes(const lh_cache* c) { return (int64_t)c->B * c->H * c->width * c->page * 4; }
@@ -195,6 +197,8 @@ lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_
   if (count != 1 && count != 2) return fail(LH_ERR_INVALID_ARG, "count must be 1 or 2");
   if (!X || !Y) return fail(LH_ERR_INVALID_ARG, "X or Y is null");
   if (B == 0 || N == 0) return ok();
+  if (!positions && (start < -(int64_t(1) << 31) || start > (int64_t(1) << 31) - N))
+    return fail(LH_ERR_INVALID_ARG, "positions must fit 32 bits");
   RowsArg x[2] = {}, y[2] = {};
   for (int i = 0; i < count; ++i) {
     LH_TRY(check_rows(X + i, "X", B, N, dtype, false, plan->c.d));
@@ -203,6 +207,7 @@ lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_
     x[i] = rows_arg(X + i);
     y[i] = rows_arg(Y + i);
   }
+  if (count == 2 && Y[0].ptr == Y[1].ptr) return fail(LH_ERR_INVALID_ARG, "Y: the two outputs overlap");
   if (x[0].H + x[1].H > 65535) return fail(LH_ERR_UNSUPPORTED, "more than 65535 heads");
   if (positions) {
     LH_CHECK_INDEX(positions);
@@ -261,7 +266,7 @@ lh_status lh_decode(const lh_cache* cache, const lh_rows* Q, float scale, void* 
   LH_TRY(check_cache(cache));
   LH_TRY(check_rows(Q, "Q", cache->B, 1, cache->dtype, false, cache->d));
   LH_TRY(check_heads(cache, Q->H, weights != nullptr));
-  if (!isfinite(scale)) return fail(LH_ERR_INVALID_ARG, "scale must be finite");
+  if (!isfinite(scale * 2.f)) return fail(LH_ERR_INVALID_ARG, "scale must be finite and below 2^127");
   LH_CHECK_PTR(O);
   LH_CHECK_INDEX(lse);
   if ((weights == nullptr) != (weights_out == nullptr))

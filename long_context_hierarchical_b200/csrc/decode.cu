@@ -187,7 +187,7 @@ struct QuadCore {
 #pragma unroll
           for (int e = 0; e < NC * EPC; ++e) o[i][e] *= f;
         }
-        const float p = live ? exp2f(sc[i] - m[i]) : 0.f;
+        const float p = live && sc[i] != -INFINITY ? exp2f(sc[i] - m[i]) : 0.f;
         l[i] += p;
 #pragma unroll
         for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * element(vc, e);
@@ -394,7 +394,7 @@ struct MmaCore {
       for (int i = 0; i < NT; ++i) {
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = (e < 2 ? live0 : live1) ? exp2_approx(x[i][e] - m[i][e & 1]) : 0.f;
+        for (int e = 0; e < 4; ++e) p[e] = x[i][e] == -INFINITY ? 0.f : exp2_approx(x[i][e] - m[i][e & 1]);
         l[i][0] += p[0] + p[2];
         l[i][1] += p[1] + p[3];
         // Rounded to bf16 as an operand: half a step, 2^-8, of each probability.
@@ -538,8 +538,8 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
       }
       if (whole) {
         const int64_t row = (int64_t)b * k.Hq + s.head0 + g;
-        static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? acc / tot : 0.f);
-        if (e == 0) k.lse[row] = tot > 0.f ? (top + log2f(tot)) * kLn2 : -INFINITY;
+        static_cast<T*>(k.o)[row * D + e] = (T)(tot == 0.f ? 0.f : acc / tot);
+        if (e == 0) k.lse[row] = tot == 0.f ? -INFINITY : (top + log2f(tot)) * kLn2;
       } else {
         part_out[g * (D + 4) + e] = acc;
         if (e == 0) {
@@ -678,8 +678,8 @@ join_kernel(const __grid_constant__ DecodeCall k) {
         tot += f * s_l[w];
         v += f * s_acc[w][e];
       }
-      static_cast<T*>(k.o)[row * D + e] = (T)(tot > 0.f ? v / tot : 0.f);
-      if (e == 0) k.lse[row] = tot > 0.f ? (top + log2f(tot)) * kLn2 : -INFINITY;
+      static_cast<T*>(k.o)[row * D + e] = (T)(tot == 0.f ? 0.f : v / tot);
+      if (e == 0) k.lse[row] = tot == 0.f ? -INFINITY : (top + log2f(tot)) * kLn2;
     }
     return;
   }

@@ -163,6 +163,13 @@ def test_rotary_refusals():
     assert call_rotary(x=rows(H=0)) == bad
     assert call_rotary(positions=ctypes.c_void_p(GOOD + 2)) == bad
     assert call_rotary(positions=ctypes.c_void_p(GOOD), stride=-1) == bad
+    two = (lh.LhRows * 2)(rows(ptr=GOOD << 4), rows(ptr=GOOD << 4))
+    assert lh.LIB.lh_rotary(ctypes.byref(lh.rotary_plan(64).raw), lh.LH_BF16, 2, 8, 2,
+                            ctypes.byref((lh.LhRows * 2)(rows(), rows(ptr=GOOD << 1))), ctypes.byref(two), None, 0,
+                            0, 0, None) == bad
+    for start in (2 ** 31 - 7, -2 ** 31 - 1):
+        assert lh.LIB.lh_rotary(ctypes.byref(lh.rotary_plan(64).raw), lh.LH_BF16, 2, 8, 1, ctypes.byref(rows()),
+                                ctypes.byref(rows(ptr=GOOD << 4)), None, 0, start, 0, None) == bad
     assert call_rotary(N=0) == lh.LH_OK and call_rotary(B=0) == lh.LH_OK   # nothing to do
 
 
@@ -176,6 +183,7 @@ def test_rotary_refusals():
     (dict(lengths=GOOD + 2), lh.LH_ERR_INVALID_ARG), (dict(table_stride=-4), lh.LH_ERR_INVALID_ARG),
     (dict(width=1 << 15, page=1 << 16), lh.LH_ERR_UNSUPPORTED),     # capacity 2^31
     (dict(B=65536, H=1), lh.LH_ERR_UNSUPPORTED),
+    (dict(v=GOOD), lh.LH_ERR_INVALID_ARG), (dict(v=GOOD + 4096), lh.LH_ERR_INVALID_ARG),   # on one another
 ])
 def test_cache_refusals(kw, status):
     c = cache(**kw)
@@ -224,7 +232,8 @@ def test_decode_refusals():
         return lh.LIB.lh_decode(ctypes.byref(c), ctypes.byref(q), scale, o, lse, w, wo, ws, n, None)
 
     assert call(q=rows(H=3)) == bad and call(q=rows(H=4, sh=20)) == bad
-    assert call(scale=float("inf")) == bad and call(o=None) == bad and call(lse=None) == bad
+    assert call(scale=float("inf")) == bad and call(scale=3e38) == bad and call(scale=float("nan")) == bad
+    assert call(o=None) == bad and call(lse=None) == bad
     assert call(w=p) == bad and call(wo=p) == bad
     assert call(w=p, wo=ctypes.c_void_p(GOOD + 64)) == bad      # shifted: overlaps
     assert call(ws=None) == bad

@@ -355,6 +355,31 @@ def test_decode_strided_queries():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_shows_a_nan_and_survives_an_overflow(dtype):
+    """A NaN in a row that is attended to reaches the head's output, and no other
+    head's; scores that overflow to -inf weigh nothing (the first keys among
+    them, where no finite score has been met yet)."""
+    from long_context_hierarchical_b200 import lh
+    c = Case([200, 200], 2, 64, 64, dtype, seed=4)
+    q = normal(c.g, (2, 4, 1, 64), dtype)
+    want = lh.decode(c.cache, c.table, c.lengths, q)
+    c.k[int(c.table[0, 1]), 1, 5, 7] = float("nan")
+    o, lse = lh.decode(c.cache, c.table, c.lengths, q)
+    assert torch.isnan(lse[0, 2:]).all() and torch.isnan(o[0, 2:]).all()
+    assert torch.equal(o[0, :2], want[0][0, :2]) and torch.equal(o[1], want[0][1])
+    q = torch.zeros_like(q)
+    q[..., 0] = 2.0
+    c.k[int(c.table[0, 0])] = 0.0
+    c.k[int(c.table[0, 0]), :, :17, 0] = -3e38
+    ones = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    o, lse = lh.decode(c.cache, c.table, ones, q, scale=1e3)
+    for h in range(4):
+        assert abs(lse[0, h, 0].item() - math.log(23)) <= 2.0 ** -20
+        mean = np64(c.rows(c.v, 0))[h // 2, 17:40].mean(0)
+        assert np.abs(np64(o[0, h, 0]) - mean).max() <= 2.0 ** -7 * np.abs(np64(c.rows(c.v, 0))[h // 2, 17:40]).max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_outside_the_cache_are_left_out_and_reported(dtype):
     from long_context_hierarchical_b200 import lh
     c = Case([100, 40], 2, 64, 16, dtype, seed=5)
