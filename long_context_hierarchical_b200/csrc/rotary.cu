@@ -16,6 +16,13 @@ namespace lh {
 namespace {
 
 constexpr int kRotThreads = 256;
+// Heads of a thread in flight, 64 bytes of each, and blocks an SM that the registers
+// are shared out for.  Measured in a graph (98,304 tokens of 8 + 2 heads of 128
+// channels, bf16; 2 x 8191 of 8 + 8 of 64, fp32): 79 and 26 us; four heads and half
+// the blocks 87 and 28 us, two heads in fp32 33 us (spills).
+constexpr int kRotBlocks = 4;
+template <typename T>
+constexpr int kInFlight = sizeof(T) == 2 ? 2 : 1;
 
 struct RotaryCall {
   RowsArg x[2], y[2];
@@ -26,13 +33,12 @@ struct RotaryCall {
   bool transpose;
 };
 
-// Two heads of a thread are in flight, with registers for four blocks an SM (three
-// in fp32): 84 us at 98,304 tokens of 8 + 2 heads of 128 channels, against 94 us
-// with four heads and half the blocks.
 template <typename T, int D>
-__global__ void __launch_bounds__(kRotThreads, sizeof(T) == 2 ? 4 : 3)
+__global__ void __launch_bounds__(kRotThreads, kRotBlocks)
 rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ RotaryCall k) {
-  constexpr int U = D / 16, kHeadsInFlight = 2;
+  constexpr int U = D / 16, kHeadsInFlight = kInFlight<T>;
+  __shared__ __align__(16) uint64_t s_turns[LH_MAX_PAIRS];
+  stage_turns(r, s_turns);
   const int64_t row = (int64_t)blockIdx.x * (kRotThreads / U) + threadIdx.x / U;
   const int u = threadIdx.x % U;
   if (row >= k.rows) return;
@@ -41,7 +47,7 @@ rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Rotar
   float c[8], s[8];
   if (unit.turn) {
     const int64_t pos = k.positions ? (int64_t)k.positions[b * k.positions_stride + n] : k.start + n;
-    unit_angles(r, u, pos, k.transpose, c, s);
+    unit_angles(r, s_turns, u, pos, k.transpose, c, s);
   }
   const int h0 = blockIdx.y * k.group;
   const int h1 = min(k.heads, h0 + k.group);
@@ -89,12 +95,12 @@ struct AppendCall {
   unsigned int* status;
 };
 
-// Four heads in flight (8192 new rows of 16 + 2 * 4 heads of 128 channels, half of
-// them padding: 53 us, against 57 us with two, which suit the rotation alone).
 template <typename T, int D>
-__global__ void __launch_bounds__(kRotThreads, 2)
+__global__ void __launch_bounds__(kRotThreads, kRotBlocks)
 append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ AppendCall k) {
-  constexpr int U = D / 16, kHeadsInFlight = 4;
+  constexpr int U = D / 16, kHeadsInFlight = kInFlight<T>;
+  __shared__ __align__(16) uint64_t s_turns[LH_MAX_PAIRS];
+  stage_turns(r, s_turns);
   const int64_t row = (int64_t)blockIdx.x * (kRotThreads / U) + threadIdx.x / U;
   const int u = threadIdx.x % U;
   if (row >= k.rows) return;
@@ -115,7 +121,7 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
   const int64_t pos = k.positions && there ? (int64_t)k.positions[b * k.positions_stride + t] : slot;
   const Unit unit = make_unit(r, u);
   float c[8], s[8];
-  if (unit.turn) unit_angles(r, u, pos, false, c, s);
+  if (unit.turn) unit_angles(r, s_turns, u, pos, false, c, s);
 
   const int Hq = k.q.H, H = k.c.H;
   const int h0 = blockIdx.y * k.group;
@@ -160,12 +166,12 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
   }
 }
 
-// Heads that one block takes: all of them where the rows alone fill the GPU
-// (the sines and cosines are then formed once), fewer for few rows.  8191 rows
-// of two sequences, fp32: 31 us with four blocks an SM, 41 with 16.
+// Heads that one block takes: all of them where the rows alone make twelve blocks
+// for each SM (the sines and cosines are then formed once), fewer for few rows.
+// 98,304 rows of 16 + 16 heads: 124 us in two groups, 127 us in one.
 int head_group(int64_t blocks, int heads) {
   int g = heads;
-  while (g > 1 && blocks * ((heads + g - 1) / g) < 148 * 4) g = (g + 1) / 2;
+  while (g > 1 && blocks * ((heads + g - 1) / g) < 148 * 12) g = (g + 1) / 2;
   return g;
 }
 

@@ -44,16 +44,24 @@ __device__ __forceinline__ Unit make_unit(const RotaryArg& r, int u) {
   return x;
 }
 
+// The frequencies in shared memory: a thread reads eight of its own, which as an
+// indexed kernel argument would be one access for each unit in the warp.
+__device__ __forceinline__ void stage_turns(const RotaryArg& r, uint64_t* s_turns) {
+  if (threadIdx.x < r.units * 8) s_turns[threadIdx.x] = r.turns[threadIdx.x];
+  __syncthreads();
+}
+
 // Sines and cosines of the unit's eight pairs.  The angle is a 64-bit fraction
 // of a turn: position * turns wraps modulo one turn exactly (negative
-// positions too), so the reduction costs no digits at any position, and what
-// is left in [-1/2, 1/2) turns is converted once to fp32.
-__device__ __forceinline__ void unit_angles(const RotaryArg& r, int u, int64_t pos, bool transpose,
-                                            float (&c)[8], float (&s)[8]) {
+// positions too), so the reduction costs no digits at any position.  Its upper 32
+// bits, in [-1/2, 1/2) turns and cut off by at most 2^-32 of one, are then
+// converted to fp32, which rounds by up to 2^-25 of a half turn.
+__device__ __forceinline__ void unit_angles(const RotaryArg& r, const uint64_t* s_turns, int u, int64_t pos,
+                                            bool transpose, float (&c)[8], float (&s)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const long long phase = (long long)((uint64_t)pos * r.turns[u * 8 + j]);
-    const float half_turns = __ll2float_rn(phase) * 0x1p-63f;
+    const int phase = (int)((uint64_t)pos * s_turns[u * 8 + j] >> 32);
+    const float half_turns = __int2float_rn(phase) * 0x1p-31f;
     sincospif(half_turns, &s[j], &c[j]);
     c[j] *= r.magnitude;
     s[j] *= transpose ? -r.magnitude : r.magnitude;
