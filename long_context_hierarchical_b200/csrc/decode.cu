@@ -187,7 +187,8 @@ struct QuadCore {
 #pragma unroll
           for (int e = 0; e < NC * EPC; ++e) o[i][e] *= f;
         }
-        const float p = live && sc[i] != -INFINITY ? exp2f(sc[i] - m[i]) : 0.f;
+        // No finite score yet: -inf less 0, not less itself.
+        const float p = live ? exp2f(sc[i] - (m[i] == -INFINITY ? 0.f : m[i])) : 0.f;
         l[i] += p;
 #pragma unroll
         for (int e = 0; e < NC * EPC; ++e) o[i][e] += p * element(vc, e);
@@ -392,9 +393,11 @@ struct MmaCore {
       uint32_t p0[NT], p1[NT];
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
+        // A masked score is -inf; where no finite one has been met, so is m.
+        const float ref[2] = {m[i][0] == -INFINITY ? 0.f : m[i][0], m[i][1] == -INFINITY ? 0.f : m[i][1]};
         float p[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = x[i][e] == -INFINITY ? 0.f : exp2_approx(x[i][e] - m[i][e & 1]);
+        for (int e = 0; e < 4; ++e) p[e] = exp2_approx(x[i][e] - ref[e & 1]);
         l[i][0] += p[0] + p[2];
         l[i][1] += p[1] + p[3];
         // Rounded to bf16 as an operand: half a step, 2^-8, of each probability.
