@@ -161,7 +161,7 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _require(t, name: str, dtype, numel: int):
@@ -718,14 +718,19 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
 
     def call(handle):
         o = _contiguous_like(Q)
-        lse = torch.empty((B, Hq, 1), dtype=torch.float32, device=dev)
-        w = _bytes(need, dev) if ws is None else ws
+        lse = Q.new_empty((B, Hq, 1), dtype=torch.float32)
+        w = _scratch(table, need) if ws is None else ws
         if B:
             _check(LIB.lh_decode(ctypes.byref(raw), _lh_rows(Q), cache.d ** -0.5 if scale is None else scale,
-                                 _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.numel(), handle), "lh_decode")
+                                 _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.nbytes, handle), "lh_decode")
         return o, lse
 
     return _run(dev, stream, tensors, call)
+
+
+def _scratch(table, nbytes: int):
+    """At least ``nbytes`` on the table's device (16-byte aligned, like every allocation)."""
+    return table.new_empty(max(4, (nbytes + 3) // 4))
 
 
 def _slots(t, name: str, dtype, shape):
@@ -789,10 +794,10 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
         n = torch.empty_like(lengths)
         wo = torch.empty_like(weights) if weights_out is None else weights_out
         po = torch.empty_like(positions) if positions is not None and positions_out is None else positions_out
-        w = _bytes(need, dev) if ws is None else ws
+        w = _scratch(table, need) if ws is None else ws
         if B:
             _check(LIB.lh_evict(ctypes.byref(raw), budget, _ptr(weights), _ptr(positions), _ptr(protect),
-                                _ptr(wo), _ptr(po), _ptr(n), _ptr(w), w.numel(), handle), "lh_evict")
+                                _ptr(wo), _ptr(po), _ptr(n), _ptr(w), w.nbytes, handle), "lh_evict")
         return n, wo, po
 
     return _run(dev, stream, tensors, call)
