@@ -440,39 +440,57 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
 }
 
 // Moves the rows: D / 8 lanes a row, key and value 16 bytes (32 in fp32) a lane.
-// Neighbouring groups take neighbouring moves and every group one at a time:
-// with all the warps an SM holds that is enough in flight, and more rows a
-// group (2 to 8, neighbours or apart) measured slower (98K cut to half, both
-// launches, 83 us against 85 to 99).
+// Neighbouring groups take neighbouring moves, so that DRAM pages stay open.  A
+// move is a chain of three loads (slots, pages, rows): the first two of the next move
+// are asked for while the rows of this one are on their way (98K cut to half,
+// both launches in a graph: 73 us, 83 us without).  One move at a time and all the warps an SM
+// holds do as well as two to four moves and fewer warps.
+template <typename T>
+constexpr int kMoveBlocks = sizeof(T) == 2 ? 7 : 5;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 6)
+__global__ void __launch_bounds__(256, kMoveBlocks<T>)
 evict_move_kernel(const __grid_constant__ EvictCall k) {
   constexpr int L = D / 8;  // lanes of a row
   const int64_t bh = blockIdx.y;
   const int b = (int)(bh / k.c.H), h = (int)(bh % k.c.H);
   cudaGridDependencySynchronize();
   const int count = k.count[bh];
-  const int32_t* table = k.c.table + b * k.c.table_stride;
+  const int32_t* const table = k.c.table + b * k.c.table_stride;
+  const int32_t* const from = k.from + bh * k.most;
+  const int32_t* const to = k.to + bh * k.most;
   const int mask = (1 << k.page_shift) - 1;
   const int lane = threadIdx.x % L;
-  const int64_t list = bh * k.most;
-  for (int64_t i = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L; i < count; i += (int64_t)gridDim.x * (256 / L)) {
-    const int src = k.from[list + count - 1 - i], dst = k.to[list + i];
-    const int64_t ps = table[src >> k.page_shift], pd = table[dst >> k.page_shift];
+  const int step = (int)gridDim.x * (256 / L);  // moves are at most half the capacity: 32 bits hold their sums
+  int src = -1, dst = 0, ps = -1, pd = -1;
+  auto ask = [&](int i) {
+    if (i >= count) return;
+    src = from[count - 1 - i];
+    dst = to[i];
+    ps = table[src >> k.page_shift];
+    pd = table[dst >> k.page_shift];
+  };
+  int i = (int)blockIdx.x * (256 / L) + threadIdx.x / L;
+  ask(i);
+  for (; i < count; i += step) {
+    Chunk<T> kc, vc;
+    int64_t ad = -1;
     if (ps >= 0 && ps < k.c.pages && pd >= 0 && pd < k.c.pages) {
-      const int64_t as = (((ps * k.c.H + h) << k.page_shift) + (src & mask)) * D + lane * 8;
-      const int64_t ad = (((pd * k.c.H + h) << k.page_shift) + (dst & mask)) * D + lane * 8;
-      Chunk<T> kc, vc;
+      const int64_t as = ((((int64_t)ps * k.c.H + h) << k.page_shift) + (src & mask)) * D + lane * 8;
+      ad = ((((int64_t)pd * k.c.H + h) << k.page_shift) + (dst & mask)) * D + lane * 8;
       kc.load(static_cast<const T*>(k.c.k) + as);
       vc.load(static_cast<const T*>(k.c.v) + as);
-      kc.store(static_cast<T*>(k.c.k) + ad);
-      vc.store(static_cast<T*>(k.c.v) + ad);
     } else if (lane == 0) {
       atomicOr(k.status, kStatusPage);
     }
     if (lane == 0) {
-      k.weights_out[bh * k.capacity + dst] = k.moved_weight[list + count - 1 - i];
-      if (k.positions_out) k.positions_out[bh * k.capacity + dst] = k.moved_position[list + count - 1 - i];
+      k.weights_out[bh * k.capacity + dst] = k.moved_weight[bh * k.most + count - 1 - i];
+      if (k.positions_out) k.positions_out[bh * k.capacity + dst] = k.moved_position[bh * k.most + count - 1 - i];
+    }
+    ask(i + step);
+    if (ad >= 0) {
+      kc.store(static_cast<T*>(k.c.k) + ad);
+      vc.store(static_cast<T*>(k.c.v) + ad);
     }
   }
 }
