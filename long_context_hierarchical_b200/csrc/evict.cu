@@ -352,6 +352,11 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
   int32_t* const to = k.to + bh * k.most;
   int32_t* const src = k.from + bh * k.most;
   float* const mw = k.moved_weight + bh * k.most;
+  // 2 KB of the histograms, which no one reads any more, for each warp.
+  static_assert(sizeof(hist) >= kEvWarps * 2048, "three lists of 128 entries a warp");
+  int* const b_slot = reinterpret_cast<int*>(&hist[0][0]) + warp * 512;
+  float* const b_weight = reinterpret_cast<float*>(b_slot + 128);
+  int* const b_pos = b_slot + 256;
   int32_t* const mp = k.moved_position + bh * k.most;
   for (int base = wlo; base < whi; base += 128 * kAhead) {
     float x[kAhead][4];
@@ -379,6 +384,7 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
       sum -= both;
       const uint32_t eq = equal + (sum >> 16);
       const int kept_before = (int)(above + (sum & 0xffff) + min(need, eq));
+      const int row_kept = (int)(above + min(need, equal));  // rows kept before this row of 128
       above += all & 0xffff;
       equal += all >> 16;
       uint32_t kept = a;
@@ -392,7 +398,44 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
           }
         }
       }
-      if (j < whi) {
+      const int row = base + 128 * r;
+      if (row + 128 <= whi && (row + 128 <= m || row >= m)) {
+        // A full row on one side of m.  Its entries are gathered in shared memory and
+        // stored side by side: a lane's own 4-byte stores would touch each sector of
+        // a list several times.
+        const bool low = row < m;
+        const uint32_t mine = low ? ~kept & 15u : kept;
+        int at = low ? (j - row) - (kept_before - row_kept) : kept_before - row_kept;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (mine >> i & 1) {
+            b_slot[at] = j + i;
+            if (!low) {
+              b_weight[at] = x[r][i];
+              if (POS) b_pos[at] = y[r][i];
+            }
+            ++at;
+          }
+        }
+        __syncwarp();
+        const int moved = (int)(above + min(need, equal)) - row_kept;
+        if (low) {
+          for (int t = lane; t < 128 - moved; t += 32) to[row - row_kept + t] = b_slot[t];
+          *reinterpret_cast<float4*>(wo + j) = make_float4(x[r][0], x[r][1], x[r][2], x[r][3]);
+          if (POS) *reinterpret_cast<int4*>(po + j) = make_int4(y[r][0], y[r][1], y[r][2], y[r][3]);
+        } else {
+          if (row == m && lane == 0) k.count[bh] = m - row_kept;
+          for (int t = lane; t < moved; t += 32) {
+            const int to_last = m - 1 - row_kept - t;
+            src[to_last] = b_slot[t];
+            mw[to_last] = b_weight[t];
+            if (POS) mp[to_last] = b_pos[t];
+          }
+          *reinterpret_cast<float4*>(wo + j) = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (POS) *reinterpret_cast<int4*>(po + j) = make_int4(-1, -1, -1, -1);
+        }
+        __syncwarp();
+      } else if (j < whi) {
         const uint32_t valid = (1u << min(4, whi - j)) - 1;
         const uint32_t low = j + 4 <= m ? 15u : j >= m ? 0u : (1u << (m - j)) - 1;  // slots below m
         if (m >= j && m < j + 4 && m < whi) k.count[bh] = m - kept_before - __popc(kept & low);
@@ -539,10 +582,10 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   k.status = device_status_ptr();
   if (!k.status) return cudaErrorInvalidSymbol;
   k.page_shift = __builtin_ctz(c.page);
-  // Blocks of a head: one for each 4096 slots, as long as every block has an SM of
-  // its own (15 clusters of eight fit side by side, 33 of four; at 16 heads of
-  // 98K slots eight blocks a head put two on some SMs, and those took 35 us where the others
-  // took 24).
+  // Blocks of a head: a power of two, one for each 4096 slots, as long as every
+  // block has an SM of its own (15 clusters of eight fit side by side, 33 of
+  // four).  16 heads of 98K slots, both launches in a graph: 74 us with four blocks a
+  // head, 77 with eight (two on some SMs), 84 with seven.
   int cs = 1;
   while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 120) cs *= 2;
   const int64_t chunk = (k.capacity + cs * 128 - 1) / (cs * 128) * 128;
