@@ -447,31 +447,26 @@ def _on_device(dev, names, tensors):
             raise ValueError(f"{names.split()[i]}: on {t.device}, the call runs on {dev}")
 
 
-def _strided(t, name: str, dtype, shape):
-    """Check a [B, H, N, d] tensor that the library reads or writes by its strides."""
+def _rows_of(t, name: str, dtype, B, H, N, d):
+    """Check a [B, H, N, d] tensor (any H where H is None) that the library reads
+    or writes by its strides; returns the five fields of its lh_rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     have = t.shape
-    if len(have) != 4 or have[0] != shape[0] or have[2] != shape[2] or have[3] != shape[3] or \
-            (shape[1] is not None and have[1] != shape[1]):
-        want = ", ".join("*" if w is None else str(w) for w in shape)
+    if have != (B, have[1] if H is None and len(have) == 4 else H, N, d):
+        want = ", ".join("*" if w is None else str(w) for w in (B, H, N, d))
         raise ValueError(f"{name}: shape {tuple(have)}, expected [{want}]")
-    if t.stride(3) != 1:
+    sb, sh, sn, sc = t.stride()
+    if sc != 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
+    return t.data_ptr(), sb, sh, sn, have[1]
 
 
-_ROWS = [None] + [_I64 * (5 * n) for n in (1, 2)]
-
-
-def _lh_rows(*tensors):
-    """One or two lh_rows (five 64-bit fields each) as a flat array."""
-    flat = []
-    for t in tensors:
-        sb, sh, sn, _ = t.stride()
-        flat += (t.data_ptr(), sb, sh, sn, t.shape[1])
-    return _ROWS[len(tensors)](*flat)
+# One to four lh_rows (five 64-bit fields each) side by side, and the bytes of one.
+_ROWS = [None] + [_I64 * (5 * n) for n in (1, 2, 3, 4)]
+_ROW_BYTES = 40
 
 
 def _index(t, name: str, shape):
@@ -507,9 +502,8 @@ class RotaryPlan:
     """Frequencies and pair layout of a rotation (from lh_rotary_init)."""
     raw: LhRotaryPlan
 
-    @property
-    def d(self):
-        return self.raw.c.d
+    def __post_init__(self):
+        self.d = self.raw.c.d
 
 
 def rotary_plan(d: int = 64, rot: int | None = None, base: float = 10000.0, layout: str = "half",
@@ -527,6 +521,12 @@ def rotary_plan(d: int = 64, rot: int | None = None, base: float = 10000.0, layo
     return RotaryPlan(raw)
 
 
+def _dense_rows(t):
+    """The lh_rows fields of a contiguous [B, H, N, d] tensor."""
+    _, H, N, d = t.shape
+    return t.data_ptr(), H * N * d, N * d, d, H
+
+
 def _contiguous_like(t):
     return torch.empty_like(t) if t.is_contiguous() else \
         torch.empty_like(t, memory_format=torch.contiguous_format)
@@ -540,21 +540,28 @@ def _rotate(rp: RotaryPlan, X, Y, positions, start, transpose, stream):
     if first.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"Q: dtype {first.dtype}, expected torch.bfloat16 or torch.float32")
     B, _, N, _ = first.shape
-    shape = (B, None, N, rp.raw.c.d)
+    d = rp.d
+    x = ()
+    y = ()
     for i, t in enumerate(X):
-        _strided(t, "QK"[i], first.dtype, shape)
+        x += _rows_of(t, "QK"[i], first.dtype, B, None, N, d)
         if Y is not None:
-            _strided(Y[i], f"out[{i}]", first.dtype, t.shape)
+            y += _rows_of(Y[i], f"out[{i}]", first.dtype, B, t.shape[1], N, d)
     stride = 0 if positions is None else _positions(positions, B, N)
     dev = first.device
     tensors = (*X, positions) if Y is None else (*X, positions, *Y)
     _on_device(dev, "Q positions out" if len(X) == 1 else "Q K positions out[0] out[1]", tensors)
 
     def call(handle):
-        out = tuple([_contiguous_like(x) for x in X]) if Y is None else Y
+        out, rows = Y, y
+        if Y is None:
+            out = tuple([_contiguous_like(t) for t in X])
+            for t in out:
+                rows += _dense_rows(t)
         if B and N:
-            _check(LIB.lh_rotary(ctypes.byref(rp.raw), _dtype_code(first), B, N, len(X), _lh_rows(*X),
-                                 _lh_rows(*out), _ptr(positions), stride, start, transpose, handle), "lh_rotary")
+            n = len(X)
+            _check(LIB.lh_rotary(ctypes.byref(rp.raw), _dtype_code(first), B, N, n, _ROWS[n](*x), _ROWS[n](*rows),
+                                 _ptr(positions), stride, start, transpose, handle), "lh_rotary")
         return out
 
     return _run(dev, stream, tensors, call)
@@ -611,19 +618,43 @@ class PagedCache:
             raise ValueError("k: expected a tensor of shape [pages, H, page, d]")
         if k.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError(f"k: dtype {k.dtype}, expected torch.bfloat16 or torch.float32")
-        _strided(v, "v", k.dtype, k.shape)
+        _rows_of(v, "v", k.dtype, *k.shape)
         for name, t in (("k", k), ("v", v)):
             if not t.is_contiguous():
                 raise ValueError(f"{name}: must be contiguous")
         if v.device != k.device:
             raise ValueError(f"v: on {v.device}, k on {k.device}")
-        self.k, self.v = k, v
+        self._k, self._v = k, v
         self.pages, self.H, self.page, self.d = k.shape
         self._c = LhCache(k.data_ptr(), v.data_ptr(), *k.shape, _dtype_code(k))
+        self._needs = {}  # bytes of scratch by the sizes of a call
+
+    @property
+    def k(self):
+        return self._k
+
+    @property
+    def v(self):
+        return self._v
 
     @property
     def dtype(self):
-        return self.k.dtype
+        return self._k.dtype
+
+    def _need(self, function, where, raw, *sizes):
+        """function(raw, *sizes), remembered: it follows from the sizes alone."""
+        key = (where, raw.B, raw.width, *sizes)
+        n = self._needs.get(key)
+        if n is None:
+            n = function(ctypes.byref(raw), *sizes)
+            if n < 0:
+                if raw.B:
+                    _check(LH_ERR_INVALID_ARG, where)
+                return 0
+            if len(self._needs) > 256:
+                self._needs.clear()
+            self._needs[key] = n
+        return n
 
     def _raw(self, table, lengths):
         """The C view of the cache with one batch's table and lengths."""
@@ -654,15 +685,12 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
     if not isinstance(K, torch.Tensor) or K.dim() != 4:
         raise ValueError("K: expected a tensor of shape [B, H, T, d]")
     raw, B, capacity = cache._raw(table, lengths)
-    T = K.shape[2]
-    shape = (B, cache.H, T, cache.d)
-    dtype = cache.k.dtype
-    _strided(K, "K", dtype, shape)
-    _strided(V, "V", dtype, shape)
+    T, H, d, k = K.shape[2], cache.H, cache.d, cache._k
+    rows = _rows_of(K, "K", k.dtype, B, H, T, d) + _rows_of(V, "V", k.dtype, B, H, T, d)
     if Q is not None:
-        _strided(Q, "Q", dtype, (B, None, T, cache.d))
+        rows += _rows_of(Q, "Q", k.dtype, B, None, T, d)
         if out is not None:
-            _strided(out, "out", dtype, Q.shape)
+            rows += _rows_of(out, "out", k.dtype, B, Q.shape[1], T, d)
     elif out is not None:
         raise ValueError("out: given without Q")
     stride = 0 if positions is None else _positions(positions, B, T)
@@ -670,19 +698,23 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
         _index(counts, "counts", (B,))
     if slot_positions is not None:
         _index(slot_positions, "slot_positions", (B, cache.H, capacity))
-    if rotary is not None and rotary.d != cache.d:
-        raise ValueError(f"rotary: for d = {rotary.d}, the cache has d = {cache.d}")
-    dev = cache.k.device
-    tensors = (cache.k, cache.v, K, V, table, lengths, positions, counts, slot_positions, Q, out)
+    if rotary is not None and rotary.d != d:
+        raise ValueError(f"rotary: for d = {rotary.d}, the cache has d = {d}")
+    dev = k.device
+    tensors = (k, cache._v, K, V, table, lengths, positions, counts, slot_positions, Q, out)
     _on_device(dev, "cache cache K V table lengths positions counts slot_positions Q out", tensors)
 
     def call(handle):
-        qo = _contiguous_like(Q) if Q is not None and out is None else out
+        qo, fields = out, rows
+        if Q is not None and out is None:
+            qo = _contiguous_like(Q)
+            fields += _dense_rows(qo)
         if T and B:
-            _check(LIB.lh_cache_append(ctypes.byref(raw), None if rotary is None else ctypes.byref(rotary.raw),
-                                       T, _lh_rows(K), _lh_rows(V), None if Q is None else _lh_rows(Q),
-                                       None if Q is None else _lh_rows(qo), _ptr(positions), stride,
-                                       _ptr(counts), _ptr(slot_positions), handle), "lh_cache_append")
+            r = _ROWS[len(fields) // 5](*fields)
+            at = [ctypes.byref(r, _ROW_BYTES * i) for i in range(len(fields) // 5)] + [None, None]
+            plan = None if rotary is None else ctypes.byref(rotary.raw)
+            _check(LIB.lh_cache_append(ctypes.byref(raw), plan, T, *at[:4], _ptr(positions), stride, _ptr(counts),
+                                       _ptr(slot_positions), handle), "lh_cache_append")
         return (qo,)
 
     return _run(dev, stream, tensors, call)[0]
@@ -699,8 +731,9 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
     ws: a uint8 scratch tensor of decode_ws_bytes(); calls that overlap on the
     GPU need one each (default: a new one)."""
     raw, B, capacity = cache._raw(table, lengths)
-    _strided(Q, "Q", cache.k.dtype, (B, None, 1, cache.d))
-    Hq = Q.shape[1]
+    k = cache._k
+    rows = _rows_of(Q, "Q", k.dtype, B, None, 1, cache.d)
+    Hq = rows[4]
     if weights is None and weights_out is not None:
         raise ValueError("weights_out: given without weights")
     if weights is not None:
@@ -708,12 +741,11 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
             weights_out = weights
         for name, t in (("weights", weights), ("weights_out", weights_out)):
             _slots(t, name, torch.float32, (B, cache.H, capacity))
-    dev = cache.k.device
-    need = _ws_need(LIB.lh_decode_ws_bytes(ctypes.byref(raw), Hq, 0 if weights is None else 1),
-                    "lh_decode_ws_bytes", B)
+    dev = k.device
+    need = cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", raw, Hq, 0 if weights is None else 1)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
-    tensors = (cache.k, cache.v, table, lengths, Q, weights, weights_out, ws)
+    tensors = (k, cache._v, table, lengths, Q, weights, weights_out, ws)
     _on_device(dev, "cache cache table lengths Q weights weights_out ws", tensors)
 
     def call(handle):
@@ -721,8 +753,9 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
         lse = Q.new_empty((B, Hq, 1), dtype=torch.float32)
         w = _scratch(table, need) if ws is None else ws
         if B:
-            _check(LIB.lh_decode(ctypes.byref(raw), _lh_rows(Q), cache.d ** -0.5 if scale is None else scale,
-                                 _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.nbytes, handle), "lh_decode")
+            _check(LIB.lh_decode(ctypes.byref(raw), _ROWS[1](*rows), cache.d ** -0.5 if scale is None else scale,
+                                 _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.nbytes,
+                                 handle), "lh_decode")
         return o, lse
 
     return _run(dev, stream, tensors, call)
@@ -744,16 +777,10 @@ def _slots(t, name: str, dtype, shape):
         raise ValueError(f"{name}: must be contiguous")
 
 
-def _ws_need(n: int, where: str, B: int) -> int:
-    if n < 0 and B:
-        _check(LH_ERR_INVALID_ARG, where)
-    return max(n, 0)
-
-
 def decode_ws_bytes(cache: PagedCache, table, lengths, Hq: int, with_weights: bool = False) -> int:
     """Bytes of scratch that ``decode`` needs for this batch."""
-    raw, B, _ = cache._raw(table, lengths)
-    return _ws_need(LIB.lh_decode_ws_bytes(ctypes.byref(raw), Hq, int(with_weights)), "lh_decode_ws_bytes", B)
+    raw, _, _ = cache._raw(table, lengths)
+    return cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", raw, Hq, int(with_weights))
 
 
 def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=None, protect=None,
@@ -783,11 +810,11 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
             _slots(t, name, torch.int32, shape)
     if protect is not None:
         _index(protect, "protect", (B,))
-    dev = cache.k.device
-    need = _ws_need(LIB.lh_evict_ws_bytes(ctypes.byref(raw), budget), "lh_evict_ws_bytes", B)
+    dev = cache._k.device
+    need = cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", raw, budget)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
-    tensors = (cache.k, cache.v, table, lengths, weights, weights_out, positions, positions_out, protect, ws)
+    tensors = (cache._k, cache._v, table, lengths, weights, weights_out, positions, positions_out, protect, ws)
     _on_device(dev, "cache cache table lengths weights weights_out positions positions_out protect ws", tensors)
 
     def call(handle):
@@ -805,8 +832,8 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
 
 def evict_ws_bytes(cache: PagedCache, table, lengths, budget: int) -> int:
     """Bytes of scratch that ``evict`` needs for this batch."""
-    raw, B, _ = cache._raw(table, lengths)
-    return _ws_need(LIB.lh_evict_ws_bytes(ctypes.byref(raw), budget), "lh_evict_ws_bytes", B)
+    raw, _, _ = cache._raw(table, lengths)
+    return cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", raw, budget)
 
 
 # --- whole layer --------------------------------------------------------------

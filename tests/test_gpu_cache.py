@@ -761,6 +761,88 @@ def test_calls_on_another_stream_and_two_at_once():
         lh.rotary(rp, x.cpu())
 
 
+def test_append_and_evict_on_another_stream():
+    from long_context_hierarchical_b200 import lh
+    rp = lh.rotary_plan(64)
+    sides = []
+    for other in (False, True):
+        c = Case([300, 90], 2, 64, 16, "bf16", seed=31)
+        new = normal(c.g, (2, 2, 20, 64), "bf16")
+        w = make_weights(c, "spread")
+        stream = torch.cuda.Stream() if other else None
+        torch.cuda.synchronize()
+        q = lh.cache_append(c.cache, c.table, c.lengths, new, new, Q=new, rotary=rp, stream=stream)
+        got = lh.evict(c.cache, c.table, c.lengths, w, 64, stream=stream)
+        junk = [torch.full((1 << 16,), float(i), device="cuda") for i in range(8)]   # the current stream goes on
+        torch.cuda.synchronize()
+        del junk
+        sides.append((q, got[0], got[1], c.k.nan_to_num(9.0), c.v.nan_to_num(9.0)))
+    for a, b in zip(*sides):
+        assert torch.equal(a, b)
+
+
+def test_two_captured_graphs_at_once():
+    """Each capture has its own workspace, so two graphs may run side by side."""
+    from long_context_hierarchical_b200 import lh
+    cases = [Case([5000, 700], 2, 64, 64, "bf16", seed=40 + i) for i in range(2)]
+    qs = [normal(c.g, (2, 4, 1, 64), "bf16") for c in cases]
+    ws = [make_weights(c, "spread") for c in cases]
+    want = [lh.decode(c.cache, c.table, c.lengths, q) for c, q in zip(cases, qs)]
+    cut = [lh.evict(lh.PagedCache.of(c.k.clone(), c.v.clone()), c.table, c.lengths, w, 600)[1]
+           for c, w in zip(cases, ws)]
+    graphs, outs, keep = [], [], []
+    for c, q, w in zip(cases, qs, ws):
+        copy = lh.PagedCache.of(c.k.clone(), c.v.clone())
+        keep.append(copy)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append((*lh.decode(c.cache, c.table, c.lengths, q),
+                         lh.evict(copy, c.table, c.lengths, w, 600)[1]))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w, e in zip(outs, want, cut):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1]) and torch.equal(o[2], e)
+
+
+def test_calls_without_rows():
+    from long_context_hierarchical_b200 import lh
+    c = Case([20, 0], 2, 64, 16, "bf16")
+    k0 = c.k.clone()
+    none = torch.zeros((2, 2, 0, 64), dtype=torch.bfloat16, device="cuda")
+    assert lh.cache_append(c.cache, c.table, c.lengths, none, none, Q=none, rotary=lh.rotary_plan(64)).shape == none.shape
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    one = normal(c.g, (2, 2, 1, 64), "bf16")
+    q = lh.cache_append(c.cache, c.table, c.lengths, one, one, Q=one, counts=zero)
+    assert not q.any() and torch.equal(c.k.nan_to_num(9.0), k0.nan_to_num(9.0))
+    empty = torch.zeros((0, 3), dtype=torch.int32, device="cuda")
+    o, lse = lh.decode(c.cache, empty, zero[:0], one[:0, :, :, :])
+    assert o.shape == (0, 2, 1, 64) and lse.shape == (0, 2, 1)
+    n, w, p = lh.evict(c.cache, empty, zero[:0], torch.zeros((0, 2, 48), device="cuda"), 5)
+    assert n.shape == (0,) and w.shape == (0, 2, 48) and p is None
+    lh.device_status()
+
+
+def test_tensors_of_a_device_that_is_not_current():
+    from long_context_hierarchical_b200 import lh
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    rp = lh.rotary_plan(64)
+    x = torch.randn(1, 2, 70, 64, device="cuda:1")
+    got = lh.rotary(rp, x)
+    assert got.device == x.device and torch.equal(got.cpu(), lh.rotary(rp, x.to("cuda:0")).cpu())
+    with pytest.raises(ValueError):
+        lh.rotary(rp, x, x.to("cuda:0"))
+    with pytest.raises(ValueError):
+        lh.rotary(rp, x, stream=torch.cuda.Stream("cuda:0"))
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^31 elements: rows at its far end are found."""
     from long_context_hierarchical_b200 import lh
