@@ -30,7 +30,6 @@ constexpr int kTile = 64;       // slots of a key tile: the unit of the split
 constexpr int kWarps = 4;       // warps of a block
 constexpr int kDecThreads = kWarps * 32;
 constexpr int kJoinThreads = 128;
-constexpr int kMaxBlocks = 148 * 5;  // ranges at most: every block of a core is resident
 constexpr int kJoinSlots = 512;   // slots whose weights one join block adds, four a thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -94,18 +93,25 @@ struct Segment {
 // each of kParts groups of keys and each head, the unnormalised output, the
 // reference m and the sum l.
 
-// Keys handled by a quad of lanes: lane r*4 + c holds channels of key r (of
+// Word i (a constant where it is called) of a 16-byte chunk.
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// fp32, on the CUDA cores: keys handled by a quad of lanes.  Lane r*4 + c holds channels of key r (of
 // the eight of a warp tile), in chunks of 16 bytes c, c + 4, ...; it keeps q and
 // the running output of GT heads for those channels, so scores take two
 // shuffles and the outputs none until the end of a segment.  GW warps share a
-// tile where the heads are more than GT.
-template <typename T_, int D_, int GT, int GW>
+// tile where the heads are more than GT.  Bound by the latency of its loads where
+// a block has few tiles (2 sequences of 8191 slots, 8 heads with weights: 17 us of the 11 that the
+// bytes take); a ring of asynchronous copies in shared memory, four tiles deep, took 22.
+template <int D_, int GT, int GW>
 struct QuadCore {
-  using T = T_;
+  using T = float;
   static constexpr int D = D_, kParts = kWarps / GW, kHeads = GT * GW;
   static constexpr int kBlocks = D == 64 ? (GT == 1 ? 4 : GT == 2 ? 3 : 2) : (GT == 1 ? 3 : 2);
-  static constexpr int EPC = 16 / sizeof(T);  // elements of a 16-byte chunk
-  static constexpr int NC = D / 4 / EPC;      // chunks of a lane
+  static constexpr int EPC = 4;            // elements of a 16-byte chunk
+  static constexpr int NC = D / 4 / EPC;  // chunks of a lane
 
   static __device__ __forceinline__ void run(const DecodeCall& k, const Segment& s, float (*sm)[kHeads][D + 4]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -125,7 +131,7 @@ struct QuadCore {
       for (int j = 0; j < NC; ++j) {
 #pragma unroll
         for (int e = 0; e < EPC; ++e) {
-          q[i][j * EPC + e] = (float)p[(c4 + 4 * j) * EPC + e] * k.scale;
+          q[i][j * EPC + e] = p[(c4 + 4 * j) * EPC + e] * k.scale;
           o[i][j * EPC + e] = 0.f;
         }
       }
@@ -150,11 +156,7 @@ struct QuadCore {
         if (at >= 0) c[i] = __ldg(reinterpret_cast<const uint4*>(p + at) + 4 * i);
       }
     };
-    auto element = [](const uint4 (&c)[NC], int e) -> float {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(c);
-      if constexpr (sizeof(T) == 2) return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
-      else return __uint_as_float(w[e]);
-    };
+    auto element = [](const uint4 (&c)[NC], int e) { return __uint_as_float(word(c[e / 4], e % 4)); };
     // K of the next tile is asked for as soon as the scores are formed, V as soon
     // as it is used.
     int64_t at = place(s.j0 + kw * 8 + r);
@@ -261,9 +263,6 @@ __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* p) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
-}
-__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 template <int D_, int NT>
@@ -754,16 +753,16 @@ void with_core(int dtype, int d, int gv, F&& f) {
       else f.template operator()<MmaCore<128, 2>>();
     }
   } else if (d == 64) {
-    if (gv == 1) f.template operator()<QuadCore<float, 64, 1, 1>>();
-    else if (gv == 2) f.template operator()<QuadCore<float, 64, 2, 1>>();
-    else if (gv <= 4) f.template operator()<QuadCore<float, 64, 2, 2>>();
-    else if (gv <= 8) f.template operator()<QuadCore<float, 64, 2, 4>>();
-    else f.template operator()<QuadCore<float, 64, 4, 4>>();
+    if (gv == 1) f.template operator()<QuadCore<64, 1, 1>>();
+    else if (gv == 2) f.template operator()<QuadCore<64, 2, 1>>();
+    else if (gv <= 4) f.template operator()<QuadCore<64, 2, 2>>();
+    else if (gv <= 8) f.template operator()<QuadCore<64, 2, 4>>();
+    else f.template operator()<QuadCore<64, 4, 4>>();
   } else {
-    if (gv == 1) f.template operator()<QuadCore<float, 128, 1, 1>>();
-    else if (gv == 2) f.template operator()<QuadCore<float, 128, 2, 1>>();
-    else if (gv <= 4) f.template operator()<QuadCore<float, 128, 2, 2>>();
-    else f.template operator()<QuadCore<float, 128, 2, 4>>();
+    if (gv == 1) f.template operator()<QuadCore<128, 1, 1>>();
+    else if (gv == 2) f.template operator()<QuadCore<128, 2, 1>>();
+    else if (gv <= 4) f.template operator()<QuadCore<128, 2, 2>>();
+    else f.template operator()<QuadCore<128, 2, 4>>();
   }
 }
 
