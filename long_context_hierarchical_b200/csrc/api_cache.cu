@@ -207,7 +207,8 @@ lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_
     x[i] = rows_arg(X + i);
     y[i] = rows_arg(Y + i);
   }
-  if (count == 2 && Y[0].ptr == Y[1].ptr) return fail(LH_ERR_INVALID_ARG, "Y: the two outputs overlap");
+  if (count == 2 && (Y[0].ptr == Y[1].ptr || Y[0].ptr == X[1].ptr || Y[1].ptr == X[0].ptr))
+    return fail(LH_ERR_INVALID_ARG, "Y: an output overlaps another tensor of the call");
   if (x[0].H + x[1].H > 65535) return fail(LH_ERR_UNSUPPORTED, "more than 65535 heads");
   if (positions) {
     LH_CHECK_INDEX(positions);

@@ -163,10 +163,11 @@ def test_rotary_refusals():
     assert call_rotary(x=rows(H=0)) == bad
     assert call_rotary(positions=ctypes.c_void_p(GOOD + 2)) == bad
     assert call_rotary(positions=ctypes.c_void_p(GOOD), stride=-1) == bad
-    two = (lh.LhRows * 2)(rows(ptr=GOOD << 4), rows(ptr=GOOD << 4))
-    assert lh.LIB.lh_rotary(ctypes.byref(lh.rotary_plan(64).raw), lh.LH_BF16, 2, 8, 2,
-                            ctypes.byref((lh.LhRows * 2)(rows(), rows(ptr=GOOD << 1))), ctypes.byref(two), None, 0,
-                            0, 0, None) == bad
+    two = (lh.LhRows * 2)(rows(), rows(ptr=GOOD << 1))
+    for outs in ((GOOD << 4, GOOD << 4), (GOOD << 1, GOOD << 4), (GOOD << 4, GOOD)):  # on one another, or exchanged
+        y = (lh.LhRows * 2)(*(rows(ptr=p) for p in outs))
+        assert lh.LIB.lh_rotary(ctypes.byref(lh.rotary_plan(64).raw), lh.LH_BF16, 2, 8, 2, ctypes.byref(two),
+                                ctypes.byref(y), None, 0, 0, 0, None) == bad
     for start in (2 ** 31 - 7, -2 ** 31 - 1):
         assert lh.LIB.lh_rotary(ctypes.byref(lh.rotary_plan(64).raw), lh.LH_BF16, 2, 8, 1, ctypes.byref(rows()),
                                 ctypes.byref(rows(ptr=GOOD << 4)), None, 0, start, 0, None) == bad

@@ -312,6 +312,16 @@ def test_decode_lengths_and_pages(dtype, page, lens):
     lh.device_status()
 
 
+@pytest.mark.parametrize("dtype,d,Hq", [("bf16", 64, 3), ("f32", 64, 1), ("bf16", 128, 12), ("f32", 128, 2)])
+def test_decode_long(dtype, d, Hq):
+    from long_context_hierarchical_b200 import lh
+    c = Case([300001, 1], 1, d, 1024, dtype, seed=d)
+    q = normal(c.g, (2, Hq, 1, d), dtype)
+    w = torch.zeros((2, 1, c.capacity), device="cuda")
+    o, lse = lh.decode(c.cache, c.table, c.lengths, q, weights=w)
+    check_decode(c, q, o, lse, weights=torch.zeros_like(w), weights_out=w)
+
+
 def test_decode_many_sequences_and_order_free():
     """More sequences than a warp holds lengths, most ranges over several of
     them; a second call gives the same bits."""
@@ -575,6 +585,44 @@ def test_evict_long():
         w[:, :, c.lens[0]:] = 0.0
         k0, v0 = c.k.clone(), c.v.clone()
         check_evict(c, w, 49152, lh.evict(c.cache, c.table, c.lengths, w, 49152), k0, v0)
+
+
+@pytest.mark.parametrize("protected", [False, True])
+@pytest.mark.parametrize("placed", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_more_slots_than_a_block_holds(protected, placed, in_place):
+    """Many heads of more slots than the selection keeps in shared memory: it
+    reads the weights again in each pass."""
+    from long_context_hierarchical_b200 import lh
+    n, H, budget, page = 41003, 64, 20000, 128
+    c = Case([n], H, 64, page, "bf16", seed=6)
+    w = make_weights(c, "ties" if protected else "spread")
+    w[:, :, n:] = 0.0
+    pos = torch.rand(w.shape, generator=c.g, device="cuda").argsort(-1).int() if placed else None
+    protect = torch.tensor([30000], dtype=torch.int32, device="cuda") if protected else None
+    k0, v0 = c.k.clone(), c.v.clone()
+    w0, p0 = w.clone(), None if pos is None else pos.clone()
+    got = lh.evict(c.cache, c.table, c.lengths, w, budget, positions=pos, protect=protect,
+                   weights_out=w if in_place else None, positions_out=pos if in_place else None)
+    assert int(got[0][0]) == budget
+    for h in (0, 17, 63):
+        _, moves, _ = oracle.evict(w0[0, h].cpu().numpy(), n, budget, None if p0 is None else p0[0, h].cpu().numpy(),
+                                   None if protect is None else 30000)
+        src, dst = (torch.tensor(x, device="cuda") for x in zip(*moves))
+        want = torch.zeros(c.capacity, device="cuda")
+        want[:budget] = w0[0, h, :budget]
+        want[dst] = w0[0, h, src]
+        assert torch.equal(got[1][0, h], want)
+        if placed:
+            p = torch.full((c.capacity,), -1, dtype=torch.int32, device="cuda")
+            p[:budget] = p0[0, h, :budget]
+            p[dst] = p0[0, h, src]
+            assert torch.equal(got[2][0, h], p)
+        table = c.table[0].long()
+        for x, x0 in ((c.k, k0), (c.v, v0)):
+            rows = x0[:, h].clone()
+            rows[table[dst // page], dst % page] = x0[table[src // page], h, src % page]
+            assert torch.equal(x[:, h].nan_to_num(9.0), rows.nan_to_num(9.0))
 
 
 def test_evict_bad_pages_move_no_rows():
