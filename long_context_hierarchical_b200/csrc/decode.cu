@@ -61,18 +61,49 @@ __device__ __forceinline__ int seq_length(const DecodeCall& k, int b) {
 
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
-// Sum over the block of one value per thread.
+// Sums over the block of two values per thread.
+struct Pair {
+  int64_t x, y;
+};
 template <int NT>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* warp_sums) {
+__device__ __forceinline__ Pair block_sum(Pair v, Pair* warp_sums) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
+  for (int o = 16; o; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
   if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
   __syncthreads();
-  int64_t t = 0;
+  Pair t{0, 0};
 #pragma unroll
-  for (int i = 0; i < NT / 32; ++i) t += warp_sums[i];
+  for (int i = 0; i < NT / 32; ++i) {
+    t.x += warp_sums[i].x;
+    t.y += warp_sums[i].y;
+  }
   return t;
+}
+
+// Sum of the values of the threads before this one, and of all.  A block's worth
+// of tile counts (less than 2^25 each) fits 32 bits.
+__device__ __forceinline__ uint32_t scan_tiles(uint32_t v, uint32_t* warp_sums, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  uint32_t before = 0;
+  *total = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    before += i < warp ? warp_sums[i] : 0;
+    *total += warp_sums[i];
+  }
+  return before + incl - v;
 }
 
 // Ranges in use and where a tile or a range lies: range c of W holds tiles
@@ -451,49 +482,58 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
   using T = typename Core::T;
   constexpr int D = Core::D, NP = Core::kParts;
   __shared__ __align__(16) float sm_o[NP][Core::kHeads][D + 4];
-  __shared__ int64_t warp_sums[kWarps];
+  __shared__ uint32_t warp_sums[kWarps];
   __shared__ int s_b;
   __shared__ int64_t s_first;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   const int Hv = k.c.H * k.nv;
   cudaTriggerProgrammaticLaunchCompletion();
 
-  for (int b = blockIdx.x; b < k.c.B; b += gridDim.x) {
-    const int len = k.c.lengths[b];
-    if (tid == 0 && (len < 0 || len > k.c.width << k.page_shift)) atomicOr(k.status, kStatusPage);
-    if (len > 0) continue;
-    for (int64_t i = tid; i < (int64_t)k.Hq * D; i += kDecThreads)
-      static_cast<T*>(k.o)[(int64_t)b * k.Hq * D + i] = (T)0.f;
-    for (int i = tid; i < k.Hq; i += kDecThreads) k.lse[(int64_t)b * k.Hq + i] = -INFINITY;
+  // Empty sequences are answered by the blocks in turn, behind their own work.
+  auto answer_empty = [&] {
+    for (int b = blockIdx.x; b < k.c.B; b += gridDim.x) {
+      const int len = k.c.lengths[b];
+      if (tid == 0 && (len < 0 || len > k.c.width << k.page_shift)) atomicOr(k.status, kStatusPage);
+      if (len > 0) continue;
+      for (int64_t i = tid; i < (int64_t)k.Hq * D; i += kDecThreads)
+        static_cast<T*>(k.o)[(int64_t)b * k.Hq * D + i] = (T)0.f;
+      for (int i = tid; i < k.Hq; i += kDecThreads) k.lse[(int64_t)b * k.Hq + i] = -INFINITY;
+    }
+  };
+  // Tiles of a key head in all sequences; those of the first 128 are kept, for most
+  // batches are no larger.
+  auto tiles = [&](int b) { return b < k.c.B ? (uint32_t)tiles_of(seq_length(k, b)) : 0u; };
+  uint32_t mine = tiles(tid), here;
+  uint32_t before = scan_tiles(mine, warp_sums, &here);
+  int64_t sum = here;
+  for (int b0 = kDecThreads; b0 < k.c.B; b0 += kDecThreads) {
+    uint32_t more;
+    scan_tiles(tiles(b0 + tid), warp_sums, &more);
+    sum += more;
   }
-  int64_t sum = 0;
-  for (int b = tid; b < k.c.B; b += kDecThreads) sum += tiles_of(seq_length(k, b));
-  const int64_t T_all = block_sum<kDecThreads>(sum, warp_sums) * Hv;
+  const int64_t T_all = sum * Hv;
   const int W = ranges(k, T_all);
-  if ((int)blockIdx.x >= W) return;
+  if ((int)blockIdx.x >= W) {
+    answer_empty();
+    return;
+  }
   int64_t u = range_begin(blockIdx.x, T_all, W);
   const int64_t u_begin = u, u_end = range_begin(blockIdx.x + 1, T_all, W);
 
-  // The sequence that tile u lies in.
-  if (tid < 32) {
-    int64_t base = 0;
-    for (int b0 = 0; b0 < k.c.B; b0 += 32) {
-      const int64_t mine = b0 + lane < k.c.B ? (int64_t)tiles_of(seq_length(k, b0 + lane)) * Hv : 0;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const int64_t before = base + incl - mine;
-      const bool hit = u >= before && u < before + mine;
-      if (hit) {
-        s_b = b0 + lane;
-        s_first = before;
-      }
-      base += __shfl_sync(0xffffffffu, incl, 31);
-      if (__any_sync(0xffffffffu, hit)) break;
+  // The sequence that tile u lies in: the one whose tiles, Hv times, enclose it.
+  const int64_t x = u / Hv;
+  int64_t base = 0;
+  for (int b0 = 0;; b0 += kDecThreads) {
+    if (b0 > 0) {
+      mine = tiles(b0 + tid);
+      before = scan_tiles(mine, warp_sums, &here);
     }
+    if (x >= base + before && x < base + before + mine) {
+      s_b = b0 + tid;
+      s_first = (base + before) * Hv;
+    }
+    base += here;
+    if (x < base) break;
   }
   __syncthreads();
   int b = s_b;
@@ -553,6 +593,7 @@ decode_kernel(const __grid_constant__ DecodeCall k) {
     __syncthreads();
     u = stop;
   }
+  answer_empty();
 }
 
 // Where the parts of a query head are: part c is the row of `of(c)`, c < count;
@@ -604,7 +645,7 @@ template <typename T, int D, int NT, bool with_weights>
 __global__ void __launch_bounds__(NT)
 join_kernel(const __grid_constant__ DecodeCall k) {
   constexpr int NW = NT / 32, E = D / 32, kClasses = 16, kPer = kClasses / NW, kChunk = 32;
-  __shared__ int64_t warp_sums[NW];
+  __shared__ Pair warp_sums[NW];
   __shared__ float s_m[kClasses], s_l[kClasses], s_acc[kClasses][D], s_lse[kChunk];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t capacity = (int64_t)k.c.width << k.page_shift;
@@ -619,15 +660,15 @@ join_kernel(const __grid_constant__ DecodeCall k) {
     return;
   }
 
-  int64_t all = 0, before = 0;
+  Pair sum{0, 0};  // tiles of a key head in all sequences, and in those before
   for (int i = tid; i < k.c.B; i += NT) {
     const int64_t t = tiles_of(seq_length(k, i));
-    all += t;
-    if (i < b) before += t;
+    sum.x += t;
+    if (i < b) sum.y += t;
   }
   const int Hv = k.c.H * k.nv;
-  const int64_t T_all = block_sum<NT>(all, warp_sums) * Hv;
-  const int64_t first = block_sum<NT>(before, warp_sums) * Hv;
+  sum = block_sum<NT>(sum, warp_sums);
+  const int64_t T_all = sum.x * Hv, first = sum.y * Hv;
   const int nt = tiles_of(n);
   const int W = ranges(k, T_all);
 
@@ -645,19 +686,33 @@ join_kernel(const __grid_constant__ DecodeCall k) {
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
     }
-#pragma unroll 2
-    for (int c = 0; c < parts.count; c += kClasses) {
+    // Many blocks (kPer > 1): few registers, so that many are resident.  Few blocks,
+    // perhaps of hundreds of parts: four parts of a class in flight (one head of 524,288
+    // slots 38 -> 30 us; with four in the other form as well, 32 ragged sequences 24 -> 28 us).
+    constexpr int kBatch = kPer == 1 ? 4 : 1;
+#pragma unroll(kPer == 1 ? 1 : 2)
+    for (int c = 0; c < parts.count; c += kClasses * kBatch) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = c + warp + NW * i;
-        if (x >= parts.count) continue;
-        const float* p = parts.of(x);
-        float v[E];
+        float v[kBatch][E], pm[kBatch], pl[kBatch];
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = p[lane + 32 * e];
-        const float2 f = merge(m[i], l[i], p[D], p[D + 1]);
+        for (int q = 0; q < kBatch; ++q) {
+          const int x = c + q * kClasses + warp + NW * i;
+          if (kBatch == 1 && x >= parts.count) continue;
+          const bool in = x < parts.count;
+          const float* p = parts.of(in ? x : 0);
+          pm[q] = in ? p[D] : -INFINITY;
+          pl[q] = in ? p[D + 1] : 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[i][e] = acc[i][e] * f.x + v[e] * f.y;
+          for (int e = 0; e < E; ++e) v[q][e] = in ? p[lane + 32 * e] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          if (kBatch == 1 && c + warp + NW * i >= parts.count) continue;
+          const float2 f = merge(m[i], l[i], pm[q], pl[q]);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[i][e] = acc[i][e] * f.x + v[q][e] * f.y;
+        }
       }
     }
 #pragma unroll
