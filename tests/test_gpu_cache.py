@@ -21,6 +21,11 @@ eps/2 of the storage type, one rounding to it):
            T = sum p |v|, S = max |s - lse| * log2(e) + 8, and lse within
            ds + (n_chain + 16) u + 4 u |lse|.  n_chain: one lane sums at most
            n / 8 keys, and the parts of all ranges.
+           That worst case would hide a single key left out of a long sequence, so
+           each row is also held in L2 norm: the roundings of the probabilities are
+           independent and spread by 2^-8 / sqrt(3) of themselves, those of the output
+           are at most H, so |O - o| <= 4 |sigma| + H |o| + |T| (the fp32 terms above)
+           with sigma_c = 2^-8 / sqrt(3) (sum_j (p_j v_jc)^2)^(1/2).
   weights  Sum of G probabilities: (2 ds + d_lse + (S + 16) u) sum p + 2 u |w + sum p|.
   evict    No arithmetic: equal.
 """
@@ -264,6 +269,12 @@ def check_decode(c, q, o, lse, scale=None, weights=None, weights_out=None, bad=(
         tol = T * rel[:, None] + HALF[dt] * np.abs(wo) * (1 + 2.0 ** -7)
         assert np.isfinite(go).all()
         assert np.all(np.abs(go - wo) <= tol), (b, np.abs(go - wo).max())
+        spread = 2.0 ** -8 / math.sqrt(3.0) if dt == torch.bfloat16 else 0.0
+        sigma = spread * np.sqrt(np.einsum("hn,hnd->hd", p * p, vr * vr))
+        norm = lambda x: np.linalg.norm(x, axis=1)  # noqa: E731
+        fp32 = 2 * ds + (2 * chain + 32) * U + S * U
+        row = 4 * norm(sigma) + HALF[dt] * norm(wo) * (1 + 2.0 ** -7) + norm(T) * fp32
+        assert np.all(norm(go - wo) <= row), (b, (norm(go - wo) / row).max())
         dl = ds + (chain + 16) * U + 4 * U * np.abs(wl)
         assert np.all(np.abs(gl - wl) <= dl), (b, np.abs(gl - wl).max())
         if weights is not None:
