@@ -21,7 +21,6 @@
 #include <algorithm>
 
 #include "host.h"
-#include "rotary.cuh"
 
 namespace lh {
 namespace {
@@ -129,13 +128,15 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
-// fp32, on the CUDA cores: keys handled by a quad of lanes.  Lane r*4 + c holds channels of key r (of
-// the eight of a warp tile), in chunks of 16 bytes c, c + 4, ...; it keeps q and
-// the running output of GT heads for those channels, so scores take two
-// shuffles and the outputs none until the end of a segment.  GW warps share a
-// tile where the heads are more than GT.  Bound by the latency of its loads where
-// a block has few tiles (2 sequences of 8191 slots, 8 heads with weights: 17 us of the 11 that the
-// bytes take); a ring of asynchronous copies in shared memory, four tiles deep, took 22.
+// fp32, on the CUDA cores: keys handled by a quad of lanes.  Lane r*4 + c holds
+// channels of key r (of the eight of a warp tile), in chunks of 16 bytes c, c + 4,
+// ...; it keeps q and the running output of GT heads for those channels, so scores
+// take two shuffles and the outputs none until the end of a segment.  GW warps
+// share a tile where the heads are more than GT.  At the copy rate on long caches
+// (16 heads of 98,304 slots: 121 us), bound by the latency of its loads where a
+// block has few tiles (2 sequences of 8191 slots, 8 heads, with weights: 17 us,
+// where the bytes take 11); a ring of asynchronous copies in shared memory, four
+// tiles deep, took 22.
 template <int D_, int GT, int GW>
 struct QuadCore {
   using T = float;
@@ -270,7 +271,9 @@ struct QuadCore {
 // asked for as soon as Sᵀ is formed, V as soon as it is used.  The work is 4 g d
 // flops per 4 d bytes, far below what even this instruction reaches, so it is
 // chosen over tcgen05, whose operands would have to pass through shared
-// memory, for its register operands.
+// memory, for its register operands.  16 heads of 98,304 slots of 64 channels take
+// 64 us in a graph, 0.97 of the copy rate; 64 ragged sequences on 4 key heads of
+// 128 channels 168 us, 0.99 (on the CUDA cores 101 and 519 us).
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"

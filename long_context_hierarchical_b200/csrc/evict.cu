@@ -22,7 +22,6 @@
 #include <algorithm>
 
 #include "host.h"
-#include "rotary.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -38,6 +37,11 @@ constexpr int kHists = 4;  // other and protected rows of the first digit, secon
 // Keys (4 bytes, and a byte for the protection of four) of a block's slots in
 // shared memory; a block with more slots reads the weights again in every pass.
 constexpr int kMaxKeys = 40960;
+constexpr int kMoveThreads = 256;
+// A head of one block whose moves are at most this many moves its rows itself.  The
+// regular cut of a batch (64 heads of 2111 slots to 2048) takes 12.4 us in a graph,
+// 12.6 with a launch for the moves, and the call 18 us instead of 21.
+constexpr int kFusedMoves = 256;
 
 struct EvictCall {
   lh_cache c;
@@ -53,6 +57,8 @@ struct EvictCall {
   unsigned int* status;
   int page_shift;
   int keys;                     // slots whose keys fit the block's shared memory
+  int row_chunks;               // 16-byte chunks of a row
+  bool fused;                   // the selecting block moves the rows itself
 };
 
 // Larger weights have larger keys; a NaN has the smallest, -0 equals +0.
@@ -60,6 +66,55 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// Moves the rows first, first + step, .. of a head's list: a group of row_chunks
+// lanes a row, 16 bytes of key and value a lane.
+// Neighbouring groups take neighbouring moves, so that DRAM pages stay open.  A
+// move is a chain of three loads (slots, pages, rows): the first two of the next
+// move are asked for while the rows of this one are on their way (98K cut to
+// half, both launches in a graph: 74 us, 83 us without).  One move at a time and
+// all the warps an SM holds do as well as two to four moves and fewer warps.
+__device__ __forceinline__ void move_rows(const EvictCall& k, int64_t bh, int first, int step) {
+  const int b = (int)(bh / k.c.H), h = (int)(bh % k.c.H);
+  const int count = k.count[bh];
+  const int32_t* const table = k.c.table + b * k.c.table_stride;
+  const int32_t* const from = k.from + bh * k.most;
+  const int32_t* const to = k.to + bh * k.most;
+  const int mask = (1 << k.page_shift) - 1;
+  const int lane = threadIdx.x & (k.row_chunks - 1);
+  uint4* const keys = static_cast<uint4*>(k.c.k);
+  uint4* const values = static_cast<uint4*>(k.c.v);
+  int src = -1, dst = 0, ps = -1, pd = -1;
+  auto ask = [&](int i) {  // moves are at most half the capacity: 32 bits hold their sums
+    if (i >= count) return;
+    src = from[count - 1 - i];
+    dst = to[i];
+    ps = table[src >> k.page_shift];
+    pd = table[dst >> k.page_shift];
+  };
+  ask(first);
+  for (int i = first; i < count; i += step) {
+    uint4 kc, vc;
+    int64_t ad = -1;
+    if (ps >= 0 && ps < k.c.pages && pd >= 0 && pd < k.c.pages) {
+      const int64_t as = ((((int64_t)ps * k.c.H + h) << k.page_shift) + (src & mask)) * k.row_chunks + lane;
+      ad = ((((int64_t)pd * k.c.H + h) << k.page_shift) + (dst & mask)) * k.row_chunks + lane;
+      kc = keys[as];
+      vc = values[as];
+    } else if (lane == 0) {
+      atomicOr(k.status, kStatusPage);
+    }
+    if (lane == 0) {
+      k.weights_out[bh * k.capacity + dst] = k.moved_weight[bh * k.most + count - 1 - i];
+      if (k.positions_out) k.positions_out[bh * k.capacity + dst] = k.moved_position[bh * k.most + count - 1 - i];
+    }
+    ask(i + step);
+    if (ad >= 0) {
+      keys[ad] = kc;
+      values[ad] = vc;
+    }
+  }
 }
 
 // A warp takes a run of its block's slots, 128 at a time, four neighbours a
@@ -480,62 +535,18 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
       }
     }
   }
+  if (k.fused) {  // a cluster of one
+    __syncthreads();
+    move_rows(k, bh, tid / k.row_chunks, kEvThreads / k.row_chunks);
+  }
 }
 
-// Moves the rows: D / 8 lanes a row, key and value 16 bytes (32 in fp32) a lane.
-// Neighbouring groups take neighbouring moves, so that DRAM pages stay open.  A
-// move is a chain of three loads (slots, pages, rows): the first two of the next move
-// are asked for while the rows of this one are on their way (98K cut to half,
-// both launches in a graph: 73 us, 83 us without).  One move at a time and all the warps an SM
-// holds do as well as two to four moves and fewer warps.
-template <typename T>
-constexpr int kMoveBlocks = sizeof(T) == 2 ? 7 : 5;
-
-template <typename T, int D>
-__global__ void __launch_bounds__(256, kMoveBlocks<T>)
+// The moves of the other calls, each row by as many lanes as it has 16-byte chunks.
+__global__ void __launch_bounds__(kMoveThreads, 7)
 evict_move_kernel(const __grid_constant__ EvictCall k) {
-  constexpr int L = D / 8;  // lanes of a row
-  const int64_t bh = blockIdx.y;
-  const int b = (int)(bh / k.c.H), h = (int)(bh % k.c.H);
   cudaGridDependencySynchronize();
-  const int count = k.count[bh];
-  const int32_t* const table = k.c.table + b * k.c.table_stride;
-  const int32_t* const from = k.from + bh * k.most;
-  const int32_t* const to = k.to + bh * k.most;
-  const int mask = (1 << k.page_shift) - 1;
-  const int lane = threadIdx.x % L;
-  const int step = (int)gridDim.x * (256 / L);  // moves are at most half the capacity: 32 bits hold their sums
-  int src = -1, dst = 0, ps = -1, pd = -1;
-  auto ask = [&](int i) {
-    if (i >= count) return;
-    src = from[count - 1 - i];
-    dst = to[i];
-    ps = table[src >> k.page_shift];
-    pd = table[dst >> k.page_shift];
-  };
-  int i = (int)blockIdx.x * (256 / L) + threadIdx.x / L;
-  ask(i);
-  for (; i < count; i += step) {
-    Chunk<T> kc, vc;
-    int64_t ad = -1;
-    if (ps >= 0 && ps < k.c.pages && pd >= 0 && pd < k.c.pages) {
-      const int64_t as = ((((int64_t)ps * k.c.H + h) << k.page_shift) + (src & mask)) * D + lane * 8;
-      ad = ((((int64_t)pd * k.c.H + h) << k.page_shift) + (dst & mask)) * D + lane * 8;
-      kc.load(static_cast<const T*>(k.c.k) + as);
-      vc.load(static_cast<const T*>(k.c.v) + as);
-    } else if (lane == 0) {
-      atomicOr(k.status, kStatusPage);
-    }
-    if (lane == 0) {
-      k.weights_out[bh * k.capacity + dst] = k.moved_weight[bh * k.most + count - 1 - i];
-      if (k.positions_out) k.positions_out[bh * k.capacity + dst] = k.moved_position[bh * k.most + count - 1 - i];
-    }
-    ask(i + step);
-    if (ad >= 0) {
-      kc.store(static_cast<T*>(k.c.k) + ad);
-      vc.store(static_cast<T*>(k.c.v) + ad);
-    }
-  }
+  const int groups = kMoveThreads / k.row_chunks;
+  move_rows(k, blockIdx.y, (int)blockIdx.x * groups + threadIdx.x / k.row_chunks, (int)gridDim.x * groups);
 }
 
 template <bool HELD>
@@ -582,12 +593,14 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   k.status = device_status_ptr();
   if (!k.status) return cudaErrorInvalidSymbol;
   k.page_shift = __builtin_ctz(c.page);
+  k.row_chunks = c.d * (c.dtype == LH_BF16 ? 2 : 4) / 16;
   // Blocks of a head: a power of two, one for each 4096 slots, as long as every
   // block has an SM of its own (15 clusters of eight fit side by side, 33 of
   // four).  16 heads of 98K slots, both launches in a graph: 74 us with four blocks a
   // head, 77 with eight (two on some SMs), 84 with seven.
   int cs = 1;
   while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 120) cs *= 2;
+  k.fused = cs == 1 && k.most <= kFusedMoves;
   const int64_t chunk = (k.capacity + cs * 128 - 1) / (cs * 128) * 128;
   k.keys = chunk <= kMaxKeys ? (int)chunk : 0;
   const size_t smem = (size_t)k.keys * 4 + k.keys / 4;
@@ -608,21 +621,18 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, select, k);
-  if (e != cudaSuccess || k.most == 0) return e;
-  with_type_dim(c.dtype, c.d, [&]<typename T, int D>() {
-    const int64_t rows = 256 / (D / 8);
-    cfg = cudaLaunchConfig_t{};
-    cfg.gridDim = dim3((unsigned)std::min<int64_t>((k.most + rows - 1) / rows, std::max<int64_t>(1, 148 * 16 / bh)),
-                       (unsigned)bh);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr + 1;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel<T, D>, k);
-  });
-  return e;
+  if (e != cudaSuccess || k.most == 0 || k.fused) return e;
+  const int64_t groups = kMoveThreads / k.row_chunks;
+  cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((k.most + groups - 1) / groups, std::max<int64_t>(1, 148 * 16 / bh)),
+                     (unsigned)bh);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = st;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr + 1;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, k);
 }
 
 }  // namespace lh

@@ -27,7 +27,7 @@ constexpr int kInFlight = sizeof(T) == 2 ? 2 : 1;
 // The unit's chunks of n heads, ss and ds elements apart, turned or copied.
 template <typename T>
 __device__ __forceinline__ void move_heads(const T* src, int64_t ss, T* dst, int64_t ds, int n, const Unit& unit,
-                                           bool turn, bool half, const float (&c)[8], const float (&s)[8]) {
+                                           bool half, const float (&c)[8], const float (&s)[8]) {
   constexpr int F = kInFlight<T>;
   const int apart = (unit.cb - unit.ca) * 8;
   src += unit.ca * 8;
@@ -45,7 +45,7 @@ __device__ __forceinline__ void move_heads(const T* src, int64_t ss, T* dst, int
     for (int i = 0; i < F; ++i) {
       if (i >= n) continue;
       T* const p = dst + i * ds;
-      if (turn) {
+      if (unit.turn) {
         float xa[8], xb[8];
         a[i].get(xa);
         e[i].get(xb);
@@ -93,7 +93,7 @@ rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Rotar
     const RowsArg &x = k.x[t], &y = k.y[t];
     const int lo = max(h0 - off, 0), hi = min(h1 - off, x.H);
     move_heads(static_cast<const T*>(x.ptr) + b * x.sb + lo * x.sh + n * x.sn, x.sh,
-               static_cast<T*>(y.ptr) + b * y.sb + lo * y.sh + n * y.sn, y.sh, hi - lo, unit, unit.turn, r.half, c, s);
+               static_cast<T*>(y.ptr) + b * y.sb + lo * y.sh + n * y.sn, y.sh, hi - lo, unit, r.half, c, s);
     off += x.H;
   }
 }

@@ -470,7 +470,7 @@ _ROW_BYTES = 40
 
 
 def _index(t, name: str, shape):
-    """Check an int32 index tensor; returns it."""
+    """Check an int32 index tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != torch.int32:
@@ -479,13 +479,10 @@ def _index(t, name: str, shape):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {list(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t
 
 
 def _positions(t, B: int, N: int):
     """Row stride of a positions tensor of shape [N], [1, N] or [B, N]."""
-    if t is None:
-        return 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"positions: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != torch.int32:
