@@ -62,7 +62,7 @@ lh_status check_rows(const lh_rows* x, const char* name, int64_t B, int64_t N, i
     if (v.size <= 1) continue;
     if (v.stride < 0) return fail(LH_ERR_INVALID_ARG, at + ": negative stride");
     if (v.stride * es % 16 != 0) return fail(LH_ERR_INVALID_ARG, at + ": rows must start on 16-byte boundaries");
-    if (v.stride > (int64_t(1) << 60) / v.size) return fail(LH_ERR_INVALID_ARG, at + ": stride too large");
+    if (v.stride > (int64_t(1) << 58) / v.size) return fail(LH_ERR_INVALID_ARG, at + ": stride too large");
   }
   if (output) {  // no two rows may overlap
     std::sort(dim, dim + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
@@ -126,7 +126,9 @@ lh_status check_cache(const lh_cache* c, bool pointers = true) {
   const void *k = c->k, *v = c->v, *table = c->table, *lengths = c->lengths;
   LH_CHECK_PTR(k); LH_CHECK_PTR(v);
   LH_CHECK_INDEX(table); LH_CHECK_INDEX(lengths);
-  const int64_t bytes = c->pages * c->H * c->page * c->d * (c->dtype == LH_BF16 ? 2 : 4);
+  const int64_t page_bytes = (int64_t)c->H * c->page * c->d * (c->dtype == LH_BF16 ? 2 : 4);
+  if (c->pages > (int64_t(1) << 60) / page_bytes) return fail(LH_ERR_INVALID_ARG, "a cache of more than 2^60 bytes");
+  const int64_t bytes = c->pages * page_bytes;
   if (k == v || !same_or_apart(k, v, bytes)) return fail(LH_ERR_INVALID_ARG, "k and v overlap");
   return LH_OK;
 }

@@ -155,6 +155,7 @@ def test_rotary_refusals():
     assert call_rotary(x=rows(ptr=GOOD + 8)) == bad and call_rotary(x=rows(ptr=None)) == bad
     assert call_rotary(x=rows(sn=68)) == bad                       # rows off the 16-byte boundary
     assert call_rotary(x=rows(sn=-64)) == bad
+    assert call_rotary(x=rows(sb=1 << 58)) == bad and b"too large" in lh.LIB.lh_last_error()
     assert call_rotary(y=rows(ptr=GOOD << 4, sn=0)) == bad         # output rows on one another
     assert b"overlap" in lh.LIB.lh_last_error()
     assert call_rotary(y=rows(ptr=GOOD << 4, sh=64 * 4)) == bad
@@ -184,6 +185,7 @@ def test_rotary_refusals():
     (dict(lengths=GOOD + 2), lh.LH_ERR_INVALID_ARG), (dict(table_stride=-4), lh.LH_ERR_INVALID_ARG),
     (dict(width=1 << 15, page=1 << 16), lh.LH_ERR_UNSUPPORTED),     # capacity 2^31
     (dict(B=65536, H=1), lh.LH_ERR_UNSUPPORTED),
+    (dict(pages=(1 << 31) - 1, H=32767, B=2, page=65536, width=1, d=128), lh.LH_ERR_INVALID_ARG),  # 2^70 bytes
     (dict(v=GOOD), lh.LH_ERR_INVALID_ARG), (dict(v=GOOD + 4096), lh.LH_ERR_INVALID_ARG),   # on one another
 ])
 def test_cache_refusals(kw, status):
