@@ -356,8 +356,8 @@ int64_t lh_cache_bytes(void); /* sizeof(lh_cache), for bindings */
  * counts[b] on are padding and are not read.  With `rotary`, K (and Q) rows are
  * turned at positions[b * positions_stride + t], or at their slot where
  * positions is NULL; without it they are copied.  Q ([B, Hq, T, d], Q and Qo
- * both or neither) goes to Qo, which may be Q itself; its padding rows become
- * zero.  slot_positions ([B, H, capacity], or NULL) receives each new slot's
+ * both or neither) goes to Qo, which may be Q itself but overlap nothing else; its
+ * padding rows become zero.  slot_positions ([B, H, capacity], or NULL) receives each new slot's
  * position.  Rows of two sequences must not share a slot of a page. */
 lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, int64_t T,
                           const lh_rows* K, const lh_rows* V, const lh_rows* Q, const lh_rows* Qo,

@@ -243,6 +243,8 @@ lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, i
     LH_TRY(check_rows(Q, "Q", B, T, cache->dtype, false, cache->d));
     LH_TRY(check_rows(Qo, "Qo", B, T, cache->dtype, true, cache->d));
     LH_TRY(check_pair(*Q, *Qo, "Q, Qo", B, T, cache->dtype, cache->d));
+    if (Qo->ptr == K->ptr || Qo->ptr == V->ptr || Qo->ptr == cache->k || Qo->ptr == cache->v)
+      return fail(LH_ERR_INVALID_ARG, "Qo: the output overlaps another tensor of the call");
     if (Q->H + 2 * cache->H > 65535) return fail(LH_ERR_UNSUPPORTED, "more than 65535 heads");
   }
   if (positions) {

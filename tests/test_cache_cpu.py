@@ -215,6 +215,8 @@ def test_append_refusals():
     assert call(K=rows(H=4, sb=4 * 512)) == bad and call(V=rows(H=1)) == bad
     assert call(Q=rows()) == bad and call(Qo=rows()) == bad
     assert call(Q=rows(), Qo=rows(ptr=GOOD + 128)) == bad
+    for q, out in ((GOOD << 4, GOOD), (GOOD << 4, c.v)):           # queries into the new keys, into the cache
+        assert call(Q=rows(ptr=q), Qo=rows(ptr=out)) == bad and b"Qo" in lh.LIB.lh_last_error()
     assert call(K=rows(sh=12)) == bad
     assert call(rotary=lh.rotary_plan(128).raw) == bad
     for name in ("counts", "positions", "slot"):
