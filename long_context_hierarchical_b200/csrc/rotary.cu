@@ -18,22 +18,19 @@ namespace {
 constexpr int kRotThreads = 256;
 // Heads of a thread in flight, 64 bytes of each, and blocks an SM that the registers
 // are shared out for.  Measured in a graph (98,304 tokens of 8 + 2 heads of 128
-// channels, bf16; 2 x 8191 of 8 + 8 of 64, fp32): 79 and 26 us; four heads and half
+// channels, bf16; 2 x 8191 of 8 + 8 of 64, fp32): 79 and 25 us; four heads and half
 // the blocks 87 and 28 us, two heads in fp32 33 us (spills).
 constexpr int kRotBlocks = 4;
 template <typename T>
 constexpr int kInFlight = sizeof(T) == 2 ? 2 : 1;
 
-// The unit's chunks of n heads, ss and ds elements apart, turned or copied.
+// A unit's chunks of the heads in flight.
 template <typename T>
-__device__ __forceinline__ void move_heads(const T* src, int64_t ss, T* dst, int64_t ds, int n, const Unit& unit,
-                                           bool half, const float (&c)[8], const float (&s)[8]) {
-  constexpr int F = kInFlight<T>;
-  const int apart = (unit.cb - unit.ca) * 8;
-  src += unit.ca * 8;
-  dst += unit.ca * 8;
-  for (; n > 0; n -= F, src += F * ss, dst += F * ds) {
-    Chunk<T> a[F], e[F];
+struct Batch {
+  static constexpr int F = kInFlight<T>;
+  Chunk<T> a[F], e[F];
+  // From src, the first of n heads ss elements apart, the chunks `apart` elements apart.
+  __device__ __forceinline__ void load(const T* src, int64_t ss, int apart, int n) {
 #pragma unroll
     for (int i = 0; i < F; ++i) {
       if (i < n) {
@@ -41,22 +38,38 @@ __device__ __forceinline__ void move_heads(const T* src, int64_t ss, T* dst, int
         e[i].load(src + i * ss + apart);
       }
     }
+  }
+};
+
+// The unit's chunks of n heads, ss and ds elements apart, turned or copied; the first
+// heads' are in x already.
+template <typename T>
+__device__ __forceinline__ void move_heads(Batch<T>& x, const T* src, int64_t ss, T* dst, int64_t ds, int n,
+                                           const Unit& unit, bool half, const float (&c)[8], const float (&s)[8]) {
+  constexpr int F = kInFlight<T>;
+  const int apart = (unit.cb - unit.ca) * 8;
+  while (true) {
 #pragma unroll
     for (int i = 0; i < F; ++i) {
       if (i >= n) continue;
       T* const p = dst + i * ds;
       if (unit.turn) {
         float xa[8], xb[8];
-        a[i].get(xa);
-        e[i].get(xb);
+        x.a[i].get(xa);
+        x.e[i].get(xb);
         turn_unit(half, c, s, xa, xb);
         Vec8<T>::store(p, xa);
         Vec8<T>::store(p + apart, xb);
       } else {
-        a[i].store(p);
-        e[i].store(p + apart);
+        x.a[i].store(p);
+        x.e[i].store(p + apart);
       }
     }
+    n -= F;
+    if (n <= 0) return;
+    src += F * ss;
+    dst += F * ds;
+    x.load(src, ss, apart, n);
   }
 }
 
@@ -80,21 +93,34 @@ rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Rotar
   if (row >= k.rows) return;
   const int64_t b = row / k.N, n = row - b * k.N;
   const Unit unit = make_unit(r, u);
+  const int apart = (unit.cb - unit.ca) * 8;
+  const int h0 = blockIdx.y * k.group;
+  const int h1 = min(k.heads, h0 + k.group);
+  // The first rows are asked for before the angles are worked out: the fp32 case above
+  // 25.1 us, 25.8 with the angles first (98,304 rows of 16 + 16 heads 123.6 and 123.2).
+  Batch<T> ahead;
+  int t = h0 >= k.x[0].H, off = t ? k.x[0].H : 0;
+  int lo = h0 - off, hi = min(h1 - off, k.x[t].H);
+  auto source = [&] { return static_cast<const T*>(k.x[t].ptr) + b * k.x[t].sb + lo * k.x[t].sh + n * k.x[t].sn + unit.ca * 8; };
+  const T* src = source();
+  ahead.load(src, k.x[t].sh, apart, hi - lo);
   float c[8], s[8];
   if (unit.turn) {
     const int64_t pos = k.positions ? (int64_t)k.positions[b * k.positions_stride + n] : k.start + n;
     unit_angles(r, s_turns, u, pos, k.transpose, c, s);
   }
-  const int h0 = blockIdx.y * k.group;
-  const int h1 = min(k.heads, h0 + k.group);
-  int off = 0;
 #pragma unroll 1
-  for (int t = 0; t < 2; ++t) {
-    const RowsArg &x = k.x[t], &y = k.y[t];
-    const int lo = max(h0 - off, 0), hi = min(h1 - off, x.H);
-    move_heads(static_cast<const T*>(x.ptr) + b * x.sb + lo * x.sh + n * x.sn, x.sh,
-               static_cast<T*>(y.ptr) + b * y.sb + lo * y.sh + n * y.sn, y.sh, hi - lo, unit, r.half, c, s);
-    off += x.H;
+  while (true) {
+    const RowsArg& y = k.y[t];
+    move_heads(ahead, src, k.x[t].sh, static_cast<T*>(y.ptr) + b * y.sb + lo * y.sh + n * y.sn + unit.ca * 8, y.sh, hi - lo,
+               unit, r.half, c, s);
+    off += k.x[t].H;
+    if (t == 1 || off >= h1) return;
+    t = 1;
+    lo = 0;
+    hi = h1 - off;
+    src = source();
+    ahead.load(src, k.x[t].sh, apart, hi);
   }
 }
 
@@ -123,6 +149,27 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
   const int64_t count = k.counts ? (int64_t)k.counts[b] : k.T;
   const int64_t capacity = (int64_t)k.c.width << k.page_shift;
   const bool there = t < count;
+  const Unit unit = make_unit(r, u);
+  const int Hq = k.q.H, H = k.c.H;
+  const int h0 = blockIdx.y * k.group;
+  const int h1 = min(Hq + 2 * H, h0 + k.group);
+  Chunk<T> a[kHeadsInFlight], e[kHeadsInFlight];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kHeadsInFlight; ++i) {
+      const int x = h + i;
+      a[i].zero();
+      e[i].zero();
+      if (x >= h1 || !there) continue;
+      const RowsArg& rows = x < Hq ? k.q : x < Hq + H ? k.k : k.v;
+      const int head = x < Hq ? x : x < Hq + H ? x - Hq : x - Hq - H;
+      const T* p = static_cast<const T*>(rows.ptr) + b * rows.sb + head * rows.sh + t * rows.sn;
+      a[i].load(p + unit.ca * 8);
+      e[i].load(p + unit.cb * 8);
+    }
+  };
+  load(h0);  // on their way while the slot's page and the angles are found (four ragged
+  // prompts of up to 8192 rows, 16 + 4 heads: 49.6 -> 48.2 us)
   const int64_t slot = (int64_t)k.c.lengths[b] - count + t;
   // A row outside the cache is left out, and so is one of a batch whose count
   // is more than the T rows that were given.
@@ -134,30 +181,13 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
   const bool bad = there && page < 0;
   if (u == 0 && blockIdx.y == 0 && (bad || (t == 0 && count < 0))) atomicOr(k.status, kStatusPage);
   const int64_t pos = k.positions && there ? (int64_t)k.positions[b * k.positions_stride + t] : slot;
-  const Unit unit = make_unit(r, u);
   float c[8], s[8];
-  if (unit.turn) unit_angles(r, s_turns, u, pos, false, c, s);
+  if (unit.turn && h0 < Hq + H) unit_angles(r, s_turns, u, pos, false, c, s);
 
-  const int Hq = k.q.H, H = k.c.H;
-  const int h0 = blockIdx.y * k.group;
-  const int h1 = min(Hq + 2 * H, h0 + k.group);
   const int64_t in_page = slot & ((1 << k.page_shift) - 1);
   // One loop over the heads of Q, K and V: a step of one row has them all in
   // flight at once (3.2 us; in three loops 3.6).
-  for (int h = h0; h < h1; h += kHeadsInFlight) {
-    Chunk<T> a[kHeadsInFlight], e[kHeadsInFlight];
-#pragma unroll
-    for (int i = 0; i < kHeadsInFlight; ++i) {
-      const int x = h + i;
-      a[i].zero();
-      e[i].zero();
-      if (x >= h1 || !there || (x >= Hq && page < 0)) continue;
-      const RowsArg& rows = x < Hq ? k.q : x < Hq + H ? k.k : k.v;
-      const int head = x < Hq ? x : x < Hq + H ? x - Hq : x - Hq - H;
-      const T* p = static_cast<const T*>(rows.ptr) + b * rows.sb + head * rows.sh + t * rows.sn;
-      a[i].load(p + unit.ca * 8);
-      e[i].load(p + unit.cb * 8);
-    }
+  for (int h = h0;;) {
 #pragma unroll
     for (int i = 0; i < kHeadsInFlight; ++i) {
       const int x = h + i;
@@ -180,12 +210,15 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
         e[i].store(out + unit.cb * 8);
       }
     }
+    h += kHeadsInFlight;
+    if (h >= h1) return;
+    load(h);
   }
 }
 
 // Heads that one block takes: all of them where the rows alone make twelve blocks
 // for each SM (the sines and cosines are then formed once), fewer for few rows.
-// 98,304 rows of 16 + 16 heads: 123 us in two groups, 127 us in one.
+// 98,304 rows of 16 + 16 heads: 124 us in two groups, 127 us in one.
 int head_group(int64_t blocks, int heads) {
   int g = heads;
   while (g > 1 && blocks * ((heads + g - 1) / g) < 148 * 12) g = (g + 1) / 2;
