@@ -209,6 +209,7 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
     for (int r = 0; r < kAhead; ++r) fetch(base + 128 * r + 4 * lane, ANY, x[r], y[r]);
 #pragma unroll
     for (int r = 0; r < kAhead; ++r) {
+      if (base + 128 * r >= whi) break;
       const int j = base + 128 * r + 4 * lane;
       uint32_t key[4], bits = 0;
 #pragma unroll
