@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -121,9 +122,9 @@ def _load():
         "lh_attn_bwd_static": (I64, I64, I32, I32, P, P, P, P, P, P, P, P, P, P),
         "lh_rotary_init": (ctypes.POINTER(LhRotaryConfig), ctypes.POINTER(LhRotaryPlan)),
         "lh_rotary": (ctypes.POINTER(LhRotaryPlan), I32, I64, I64, I32, P, P, P, I64, I64, I32, P),
-        "lh_cache_append": (ctypes.POINTER(LhCache), P, I64, P, P, P, P, P, I64, P, P, P),
-        "lh_decode": (ctypes.POINTER(LhCache), P, ctypes.c_float, P, P, P, P, P, SZ, P),
-        "lh_evict": (ctypes.POINTER(LhCache), I64, P, P, P, P, P, P, P, SZ, P),
+        "lh_cache_append": (P, P, I64, P, P, P, P, P, I64, P, P, P),
+        "lh_decode": (P, P, ctypes.c_float, P, P, P, P, P, SZ, P),
+        "lh_evict": (P, I64, P, P, P, P, P, P, P, SZ, P),
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -139,8 +140,8 @@ def _load():
     lib.lh_plan_bytes.restype = I64
     lib.lh_set_deterministic.argtypes = [ctypes.c_int]
     lib.lh_set_deterministic.restype = None
-    lib.lh_decode_ws_bytes.argtypes = [ctypes.POINTER(LhCache), I64, I32]
-    lib.lh_evict_ws_bytes.argtypes = [ctypes.POINTER(LhCache), I64]
+    lib.lh_decode_ws_bytes.argtypes = [P, I64, I32]
+    lib.lh_evict_ws_bytes.argtypes = [P, I64]
     for name in ("lh_decode_ws_bytes", "lh_evict_ws_bytes", "lh_rotary_plan_bytes", "lh_cache_bytes"):
         getattr(lib, name).restype = I64
     if lib.lh_plan_bytes() != ctypes.sizeof(LhPlan):
@@ -464,9 +465,12 @@ def _rows_of(t, name: str, dtype, B, H, N, d):
     return t.data_ptr(), sb, sh, sn, have[1]
 
 
-# One to four lh_rows (five 64-bit fields each) side by side, and the bytes of one.
-_ROWS = [None] + [_I64 * (5 * n) for n in (1, 2, 3, 4)]
-_ROW_BYTES = 40
+# An lh_rows, one or two side by side, and the two halves of an lh_cache, packed: a
+# ctypes object made for every call takes several times as long.
+_ROW = struct.Struct("P4q").pack
+_ROWS = (None, _ROW, struct.Struct("P4qP4q").pack)
+_PAGES = struct.Struct("PPq4i").pack    # k, v, pages, H, page, d, dtype
+_BATCH = struct.Struct("PqiiP").pack    # table, table_stride, B, width, lengths
 
 
 def _index(t, name: str, shape):
@@ -621,9 +625,11 @@ class PagedCache:
                 raise ValueError(f"{name}: must be contiguous")
         if v.device != k.device:
             raise ValueError(f"v: on {v.device}, k on {k.device}")
+        if any(n >> 31 for n in k.shape[1:]):
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected H, page and d below 2^31")
         self._k, self._v = k, v
         self.pages, self.H, self.page, self.d = k.shape
-        self._c = LhCache(k.data_ptr(), v.data_ptr(), *k.shape, _dtype_code(k))
+        self._c = _PAGES(k.data_ptr(), v.data_ptr(), *k.shape, _dtype_code(k))
         self._needs = {}  # bytes of scratch by the sizes of a call
 
     @property
@@ -638,14 +644,14 @@ class PagedCache:
     def dtype(self):
         return self._k.dtype
 
-    def _need(self, function, where, raw, *sizes):
+    def _need(self, function, where, raw, B, capacity, *sizes):
         """function(raw, *sizes), remembered: it follows from the sizes alone."""
-        key = (where, raw.B, raw.width, *sizes)
+        key = (where, B, capacity, *sizes)
         n = self._needs.get(key)
         if n is None:
-            n = function(ctypes.byref(raw), *sizes)
+            n = function(raw, *sizes)
             if n < 0:
-                if raw.B:
+                if B:
                     _check(LH_ERR_INVALID_ARG, where)
                 return 0
             if len(self._needs) > 256:
@@ -654,7 +660,7 @@ class PagedCache:
         return n
 
     def _raw(self, table, lengths):
-        """The C view of the cache with one batch's table and lengths."""
+        """The lh_cache of one batch's table and lengths, B and the capacity."""
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table: expected a tensor of shape [B, width]")
         if table.dtype != torch.int32:
@@ -663,10 +669,9 @@ class PagedCache:
         if width > 1 and table.stride(1) != 1:
             raise ValueError("table: a sequence's pages must be contiguous")
         _index(lengths, "lengths", (B,))
-        raw = LhCache.from_buffer_copy(self._c)
-        raw.table, raw.table_stride, raw.B, raw.width = table.data_ptr(), table.stride(0), B, width
-        raw.lengths = lengths.data_ptr()
-        return raw, B, width * self.page
+        if (B | width) >> 31:
+            raise ValueError(f"table: shape {tuple(table.shape)}, expected sizes below 2^31")
+        return self._c + _BATCH(table.data_ptr(), table.stride(0), B, width, lengths.data_ptr()), B, width * self.page
 
 
 def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: RotaryPlan | None = None,
@@ -683,11 +688,12 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
         raise ValueError("K: expected a tensor of shape [B, H, T, d]")
     raw, B, capacity = cache._raw(table, lengths)
     T, H, d, k = K.shape[2], cache.H, cache.d, cache._k
-    rows = _rows_of(K, "K", k.dtype, B, H, T, d) + _rows_of(V, "V", k.dtype, B, H, T, d)
+    new_k, new_v = _ROW(*_rows_of(K, "K", k.dtype, B, H, T, d)), _ROW(*_rows_of(V, "V", k.dtype, B, H, T, d))
+    q = to = None
     if Q is not None:
-        rows += _rows_of(Q, "Q", k.dtype, B, None, T, d)
+        q = _ROW(*_rows_of(Q, "Q", k.dtype, B, None, T, d))
         if out is not None:
-            rows += _rows_of(out, "out", k.dtype, B, Q.shape[1], T, d)
+            to = _ROW(*_rows_of(out, "out", k.dtype, B, Q.shape[1], T, d))
     elif out is not None:
         raise ValueError("out: given without Q")
     stride = 0 if positions is None else _positions(positions, B, T)
@@ -702,16 +708,14 @@ def cache_append(cache: PagedCache, table, lengths, K, V, Q=None, rotary: Rotary
     _on_device(dev, "cache cache K V table lengths positions counts slot_positions Q out", tensors)
 
     def call(handle):
-        qo, fields = out, rows
+        qo, qo_rows = out, to
         if Q is not None and out is None:
             qo = _contiguous_like(Q)
-            fields += _dense_rows(qo)
+            qo_rows = _ROW(*_dense_rows(qo))
         if T and B:
-            r = _ROWS[len(fields) // 5](*fields)
-            at = [ctypes.byref(r, _ROW_BYTES * i) for i in range(len(fields) // 5)] + [None, None]
-            plan = None if rotary is None else ctypes.byref(rotary.raw)
-            _check(LIB.lh_cache_append(ctypes.byref(raw), plan, T, *at[:4], _ptr(positions), stride, _ptr(counts),
-                                       _ptr(slot_positions), handle), "lh_cache_append")
+            _check(LIB.lh_cache_append(raw, None if rotary is None else ctypes.byref(rotary.raw), T, new_k, new_v, q,
+                                       qo_rows, _ptr(positions), stride, _ptr(counts), _ptr(slot_positions), handle),
+                   "lh_cache_append")
         return (qo,)
 
     return _run(dev, stream, tensors, call)[0]
@@ -739,7 +743,7 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
         for name, t in (("weights", weights), ("weights_out", weights_out)):
             _slots(t, name, torch.float32, (B, cache.H, capacity))
     dev = k.device
-    need = cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", raw, Hq, 0 if weights is None else 1)
+    need = cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", raw, B, capacity, Hq, 0 if weights is None else 1)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
     tensors = (k, cache._v, table, lengths, Q, weights, weights_out, ws)
@@ -750,7 +754,7 @@ def decode(cache: PagedCache, table, lengths, Q, scale: float | None = None, wei
         lse = Q.new_empty((B, Hq, 1), dtype=torch.float32)
         w = _scratch(table, need) if ws is None else ws
         if B:
-            _check(LIB.lh_decode(ctypes.byref(raw), _ROWS[1](*rows), cache.d ** -0.5 if scale is None else scale,
+            _check(LIB.lh_decode(raw, _ROW(*rows), cache.d ** -0.5 if scale is None else scale,
                                  _ptr(o), _ptr(lse), _ptr(weights), _ptr(weights_out), _ptr(w), w.nbytes,
                                  handle), "lh_decode")
         return o, lse
@@ -776,8 +780,7 @@ def _slots(t, name: str, dtype, shape):
 
 def decode_ws_bytes(cache: PagedCache, table, lengths, Hq: int, with_weights: bool = False) -> int:
     """Bytes of scratch that ``decode`` needs for this batch."""
-    raw, _, _ = cache._raw(table, lengths)
-    return cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", raw, Hq, int(with_weights))
+    return cache._need(LIB.lh_decode_ws_bytes, "lh_decode_ws_bytes", *cache._raw(table, lengths), Hq, int(with_weights))
 
 
 def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=None, protect=None,
@@ -808,7 +811,7 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
     if protect is not None:
         _index(protect, "protect", (B,))
     dev = cache._k.device
-    need = cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", raw, budget)
+    need = cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", raw, B, capacity, budget)
     if ws is not None:
         _require(ws, "ws", torch.uint8, need)
     tensors = (cache._k, cache._v, table, lengths, weights, weights_out, positions, positions_out, protect, ws)
@@ -820,7 +823,7 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
         po = torch.empty_like(positions) if positions is not None and positions_out is None else positions_out
         w = _scratch(table, need) if ws is None else ws
         if B:
-            _check(LIB.lh_evict(ctypes.byref(raw), budget, _ptr(weights), _ptr(positions), _ptr(protect),
+            _check(LIB.lh_evict(raw, budget, _ptr(weights), _ptr(positions), _ptr(protect),
                                 _ptr(wo), _ptr(po), _ptr(n), _ptr(w), w.nbytes, handle), "lh_evict")
         return n, wo, po
 
@@ -829,8 +832,7 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
 
 def evict_ws_bytes(cache: PagedCache, table, lengths, budget: int) -> int:
     """Bytes of scratch that ``evict`` needs for this batch."""
-    raw, _, _ = cache._raw(table, lengths)
-    return cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", raw, budget)
+    return cache._need(LIB.lh_evict_ws_bytes, "lh_evict_ws_bytes", *cache._raw(table, lengths), budget)
 
 
 # --- whole layer --------------------------------------------------------------
