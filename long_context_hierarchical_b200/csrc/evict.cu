@@ -39,8 +39,8 @@ constexpr int kHists = 4;  // other and protected rows of the first digit, secon
 constexpr int kMaxKeys = 40960;
 constexpr int kMoveThreads = 256;
 // A head of one block whose moves are at most this many moves its rows itself.  The
-// regular cut of a batch (64 heads of 2111 slots to 2048) takes 12.4 us in a graph,
-// 12.6 with a launch for the moves, and the call 18 us instead of 21.
+// regular cut of a batch (64 heads of 2111 slots to 2048) takes 11.7 us in a graph,
+// 0.2 more with a launch for the moves, and the call 18 us instead of 21.
 constexpr int kFusedMoves = 256;
 
 struct EvictCall {
