@@ -255,7 +255,7 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
   // Block r sums the r-th highest share of the bins; a thread takes four.
   uint32_t threshold = 0, mask = 0, need = m;
   bool active = false;  // the class (protected or not) that the threshold splits
-  const int bins = kBins / CS;
+  const int bins = CS == 1 ? kBins : (kBins + 4 * CS - 1) / (4 * CS) * 4;  // the lowest share may begin below bin 0
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
@@ -281,7 +281,7 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
         uint4 v[kMaxCluster], all = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i)
-          v[i] = i < CS ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(h, i) + at) : all;
+          v[i] = i < CS && at >= 0 ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(h, i) + at) : all;
 #pragma unroll
         for (int i = 0; i < kMaxCluster; ++i) {
           all.x += v[i].x;
@@ -290,7 +290,8 @@ evict_select_kernel(const __grid_constant__ EvictCall k) {
           all.w += v[i].w;
         }
         *reinterpret_cast<uint4*>(&share[c][4 * tid]) = all;
-        const uint32_t rows = __reduce_add_sync(__activemask(), all.x + all.y + all.z + all.w);
+        const int live = bins / 4 - (tid & ~31);  // threads of this warp with a part
+        const uint32_t rows = __reduce_add_sync(live >= 32 ? ~0u : (1u << live) - 1, all.x + all.y + all.z + all.w);
         if (lane == 0) atomicAdd(&s_rows[c], rows);
       }
     }
@@ -596,12 +597,15 @@ cudaError_t launch_evict(const lh_cache& c, int64_t budget, const float* weights
   if (!k.status) return cudaErrorInvalidSymbol;
   k.page_shift = __builtin_ctz(c.page);
   k.row_chunks = c.d * (c.dtype == LH_BF16 ? 2 : 4) / 16;
-  // Blocks of a head: a power of two, one for each 4096 slots, as long as every
-  // block has an SM of its own (15 clusters of eight fit side by side, 33 of
-  // four).  16 heads of 98K slots, both launches in a graph: 74 us with four blocks a
-  // head, 77 with eight (two on some SMs), 84 with seven.
-  int cs = 1;
-  while (cs < kMaxCluster && k.capacity > (int64_t)cs * 4096 && bh * cs * 2 <= 120) cs *= 2;
+  // Blocks of a head: one up to 4096 slots (8 heads of them: 12.6 us in a graph, 15.9 in
+  // two), behind that one for each 2048, as many as leave every block an SM of its own
+  // (kFit: clusters of one to eight that stand side by side, for none spans two parts of
+  // the GPU).  16 heads of 98K slots, both launches in a graph: 71 us with six blocks a
+  // head, 72 with four, 77 with eight and 84 with seven (two on some SMs); 32 heads of
+  // 32K slots, few to move: 26 us with four, 33 with two.
+  constexpr int kFit[kMaxCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+  int cs = k.capacity > 4096 ? kMaxCluster : 1;
+  while (cs > 1 && (bh > kFit[cs] || k.capacity <= (int64_t)(cs - 1) * 2048)) --cs;
   k.fused = cs == 1 && k.most <= kFusedMoves;
   const int64_t chunk = (k.capacity + cs * 128 - 1) / (cs * 128) * 128;
   k.keys = chunk <= kMaxKeys ? (int)chunk : 0;

@@ -598,6 +598,25 @@ def test_evict_long():
         check_evict(c, w, 49152, lh.evict(c.cache, c.table, c.lengths, w, 49152), k0, v0)
 
 
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal"])
+@pytest.mark.parametrize("H,n", [(26, 6100), (20, 6101), (14, 6102), (10, 8103), (8, 10104), (6, 12105), (1, 14106),
+                                 (5, 16507)])
+def test_evict_heads_of_one_to_eight_blocks(H, n, kind):
+    # three sequences of H heads: from many heads of one block to few of eight; the
+    # shorter sequences leave some blocks of a head without a slot
+    from long_context_hierarchical_b200 import lh
+    c = Case([n, 5, n // 2], H, 64, 16, "bf16", seed=n)
+    w = make_weights(c, kind)
+    protect = (c.lengths - 300).int()
+    for budget in (n // 3, n - 40):
+        k0, v0 = c.k.clone(), c.v.clone()
+        check_evict(c, w, budget, lh.evict(c.cache, c.table, c.lengths, w, budget, protect=protect), k0, v0, None,
+                    protect)
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+    lh.device_status()
+
+
 @pytest.mark.parametrize("protected", [False, True])
 @pytest.mark.parametrize("placed", [False, True])
 @pytest.mark.parametrize("in_place", [False, True])
