@@ -73,6 +73,13 @@ __device__ __forceinline__ void move_heads(Batch<T>& x, const T* src, int64_t ss
   }
 }
 
+// Heads of a block at most, evenly shared out.  98,304 rows of 16 + 16 heads of 64
+// channels, bf16, calls of fresh inputs: 123 us with eight, 123 with six, 127 with four
+// (the angles are formed more often) and 126 with sixteen (a block's stores reach
+// farther apart); 524,288 rows 648, 663, 680 and 660 us.  The append keeps more: a row
+// costs it its page as well as its angles (four prompts: 48 us with twelve, 50 with six).
+constexpr int kMostHeads = 8;
+
 struct RotaryCall {
   RowsArg x[2], y[2];
   const int32_t* positions;
@@ -97,7 +104,7 @@ rotary_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Rotar
   const int h0 = blockIdx.y * k.group;
   const int h1 = min(k.heads, h0 + k.group);
   // The first rows are asked for before the angles are worked out: the fp32 case above
-  // 25.1 us, 25.8 with the angles first (98,304 rows of 16 + 16 heads 123.6 and 123.2).
+  // 25.1 us, 25.8 with the angles first.
   Batch<T> ahead;
   int t = h0 >= k.x[0].H, off = t ? k.x[0].H : 0;
   int lo = h0 - off, hi = min(h1 - off, k.x[t].H);
@@ -218,7 +225,6 @@ append_kernel(const __grid_constant__ RotaryArg r, const __grid_constant__ Appen
 
 // Heads that one block takes: all of them where the rows alone make twelve blocks
 // for each SM (the sines and cosines are then formed once), fewer for few rows.
-// 98,304 rows of 16 + 16 heads: 124 us in two groups, 127 us in one.
 int head_group(int64_t blocks, int heads) {
   int g = heads;
   while (g > 1 && blocks * ((heads + g - 1) / g) < 148 * 12) g = (g + 1) / 2;
@@ -244,7 +250,8 @@ cudaError_t launch_rotary(const lh_rotary_plan& plan, int dtype, int64_t B, int6
   k.transpose = transpose;
   const int64_t per = kRotThreads / (plan.c.d / 16);
   const int64_t blocks = (k.rows + per - 1) / per;
-  k.group = head_group(blocks, k.heads);
+  const int parts = (k.heads + kMostHeads - 1) / kMostHeads;
+  k.group = std::min(head_group(blocks, k.heads), (k.heads + parts - 1) / parts);
   const dim3 grid((unsigned)blocks, (k.heads + k.group - 1) / k.group);
   const RotaryArg r = make_rotary_arg(&plan);
   with_type_dim(dtype, plan.c.d, [&]<typename T, int D>() { rotary_kernel<T, D><<<grid, kRotThreads, 0, st>>>(r, k); });
