@@ -97,6 +97,24 @@ def test_rotary_shapes(dtype, d, rot, layout, B, Hq, Hk, N):
         assert torch.equal(call(rp, q, start=11), a)   # alone: the same bits
 
 
+@pytest.mark.parametrize("dtype,d,Hq,Hk,N", [("bf16", 64, 7, 3, 120001), ("bf16", 64, 17, 1, 120001),
+                                             ("bf16", 128, 9, 2, 60001), ("f32", 64, 5, 2, 120001),
+                                             ("f32", 128, 3, 8, 60001)])
+def test_rotary_blocks_of_several_heads(dtype, d, Hq, Hk, N):
+    # rows enough for blocks of several heads, some of Q's last and K's first: the bits
+    # of each head turned alone, also in place
+    from long_context_hierarchical_b200 import lh
+    g = gen(Hq)
+    rp = lh.rotary_plan(d, rot=d // 2)
+    q, k = normal(g, (1, Hq, N, d), dtype), normal(g, (1, Hk, N, d), dtype)
+    turned = lh.rotary(rp, q, k, start=7)
+    for x, y in zip((q, k), turned):
+        for h in range(x.shape[1]):
+            assert torch.equal(y[:, h:h + 1], lh.rotary(rp, x[:, h:h + 1], start=7)), h
+    lh.rotary(rp, q, k, start=7, out=(q, k))
+    assert torch.equal(q, turned[0]) and torch.equal(k, turned[1])
+
+
 @pytest.mark.parametrize("kw", [
     dict(scaling="linear", factor=4.0), dict(scaling="bands", factor=8.0, low=1.0, high=4.0, original=8192.0),
     dict(magnitude=1.25), dict(base=500000.0)])
