@@ -266,14 +266,14 @@ struct QuadCore {
 //   V  it holds chunk r (and r + 8) of keys 2c, 2c + 1, 2c + 8, 2c + 9; a byte
 //      permute pairs two keys of one channel, channels 8r + 2w and + 1 being rows
 //      r and r + 8 of m tile w;
-//   P  the two 8 x 8 halves of Sᵀ become the B fragment by movmatrix.
+//   P  the two 8 x 8 halves of Sᵀ, in two bf16 parts, become B fragments by movmatrix.
 // No shared memory is touched until the end of a segment.  K of the next tile is
 // asked for as soon as Sᵀ is formed, V as soon as it is used.  The work is 4 g d
 // flops per 4 d bytes, far below what even this instruction reaches, so it is
 // chosen over tcgen05, whose operands would have to pass through shared
 // memory, for its register operands.  16 heads of 98,304 slots of 64 channels take
-// 64 us in a graph, 0.97 of the copy rate; 64 ragged sequences on 4 key heads of
-// 128 channels 168 us, 0.99 (on the CUDA cores 101 and 519 us).
+// 64 us in a graph, 0.98 of the copy rate; 64 ragged sequences on 4 key heads of
+// 128 channels 172 us, 0.97 (on the CUDA cores 101 and 519 us).
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
@@ -423,7 +423,7 @@ struct MmaCore {
           }
         }
       }
-      uint32_t p0[NT], p1[NT];
+      uint32_t hi[NT][2], lo[NT][2];  // B fragments
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         // A masked score is -inf; where no finite one has been met, so is m.
@@ -433,10 +433,18 @@ struct MmaCore {
         for (int e = 0; e < 4; ++e) p[e] = exp2_approx(x[i][e] - ref[e & 1]);
         l[i][0] += p[0] + p[2];
         l[i][1] += p[1] + p[3];
-        // Rounded to bf16 as an operand: half a step, 2^-8, of each probability.
-        __nv_bfloat162 lo = __floats2bfloat162_rn(p[0], p[1]), hi = __floats2bfloat162_rn(p[2], p[3]);
-        p0[i] = transpose8x8(*reinterpret_cast<uint32_t*>(&lo));
-        p1[i] = transpose8x8(*reinterpret_cast<uint32_t*>(&hi));
+        // Two bf16 operands each, a probability rounded and what that leaves of it: within 2^-16,
+        // where a single one would be off by 2^-8.  In a graph 64 ragged sequences on 4 key heads
+        // of 128 take 171.9 us, 171.1 with one operand; 8 of 16,384 slots, 16 on 1 head of 64,
+        // 32.8 us, 31.2.
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const __nv_bfloat162 big = __floats2bfloat162_rn(p[2 * e], p[2 * e + 1]);
+          const __nv_bfloat162 rest =
+              __floats2bfloat162_rn(p[2 * e] - __low2float(big), p[2 * e + 1] - __high2float(big));
+          hi[i][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&big));
+          lo[i][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&rest));
+        }
       }
 #pragma unroll
       for (int j = 0; j < VC; ++j) {
@@ -447,7 +455,10 @@ struct MmaCore {
                                  __byte_perm(word(vc[2][j], w), word(vc[3][j], w), 0x5410),
                                  __byte_perm(word(vc[2][j], w), word(vc[3][j], w), 0x7632)};
 #pragma unroll
-          for (int i = 0; i < NT; ++i) mma16816(o[i][j * 4 + w], a, p0[i], p1[i]);
+          for (int i = 0; i < NT; ++i) {
+            mma16816(o[i][j * 4 + w], a, lo[i][0], lo[i][1]);
+            mma16816(o[i][j * 4 + w], a, hi[i][0], hi[i][1]);
+          }
         }
       }
       if (next < s.j1) load_v(at_next, next);

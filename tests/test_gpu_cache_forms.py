@@ -1,0 +1,41 @@
+"""Forms of the rotary and cache calls that their users meet, on the GPU: longer, wider and
+repeated ones than the operators' own tests take.  Oracle and bounds are those of
+tests/test_gpu_cache.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oracle
+from tests.helpers import np64
+from tests.test_gpu_cache import U, Case, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,G", [(2, 1), (1, 8), (2, 12)])
+@pytest.mark.parametrize("lens", [[37, 1, 0, 200], [1500, 64]])
+def test_decode_rounds_only_what_it_stores(d, H, G, lens):
+    """bf16 outputs are as good as fp32 probabilities make them.  A probability enters
+    the product as two bf16 numbers: the first is within 2^-8 of it, the remainder is
+    exact in fp32 and the second within 2^-8 of that, so together they are within 2^-16
+    of the probability.  |O - o| <= T (2 ds + 2^-16 + (2 n_chain + 32 + S) u) + H |o| in
+    the header's terms, for every channel, small ones among them."""
+    from long_context_hierarchical_b200 import lh
+    c = Case(lens, H, d, 16, "bf16", seed=d + G)
+    q = normal(c.g, (len(lens), H * G, 1, d), "bf16")
+    o, _ = lh.decode(c.cache, c.table, c.lengths, q)
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        k, v, qb = np64(c.rows(c.k, b)), np64(c.rows(c.v, b)), np64(q[b, :, 0])
+        want, lse, p = oracle.decode(qb, k, v, d ** -0.5)
+        kr, vr = np.repeat(k, G, 0), np.repeat(v, G, 0)
+        ds = (d + 6) * U * d ** -0.5 * np.einsum("hd,hnd->hn", np.abs(qb), np.abs(kr)).max(1)
+        S = np.abs(np.einsum("hd,hnd->hn", qb, kr) * d ** -0.5 - lse[:, None]).max(1) / math.log(2.0) + 8
+        rel = 2 * ds + 2.0 ** -16 + (2 * (n / 8 + 664) + 32 + S) * U
+        tol = np.einsum("hn,hnd->hd", p, np.abs(vr)) * rel[:, None] + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
+        off = np.abs(np64(o[b, :, 0]) - want)
+        assert np.all(off <= tol), (b, (off / tol).max())
