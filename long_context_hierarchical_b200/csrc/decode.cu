@@ -273,7 +273,7 @@ struct QuadCore {
 // chosen over tcgen05, whose operands would have to pass through shared
 // memory, for its register operands.  16 heads of 98,304 slots of 64 channels take
 // 64 us in a graph, 0.98 of the copy rate; 64 ragged sequences on 4 key heads of
-// 128 channels 172 us, 0.97 (on the CUDA cores 101 and 519 us).
+// 128 channels 167 us, 1.00 (on the CUDA cores 101 and 519 us).
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
@@ -289,6 +289,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// What a probability cut off to bf16 leaves of it (exact), at least 2^-126 of a positive one.
+__device__ __forceinline__ float remainder_of(float p) {
+  return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xffff0000u), fminf(p, 0x1p-126f));
 }
 // Cache rows are read once: past L1.
 __device__ __forceinline__ uint4 load_row(const __nv_bfloat16* p) {
@@ -433,16 +437,16 @@ struct MmaCore {
         for (int e = 0; e < 4; ++e) p[e] = exp2_approx(x[i][e] - ref[e & 1]);
         l[i][0] += p[0] + p[2];
         l[i][1] += p[1] + p[3];
-        // Two bf16 operands each, a probability rounded and what that leaves of it: within 2^-16,
-        // where a single one would be off by 2^-8.  In a graph 64 ragged sequences on 4 key heads
-        // of 128 take 171.9 us, 171.1 with one operand; 8 of 16,384 slots, 16 on 1 head of 64,
-        // 32.8 us, 31.2.
+        // Two bf16 operands each, a probability cut off and what that leaves of it: within 2^-16,
+        // where a single one would be off by 2^-8.  Both are positive where the probability is,
+        // so that an infinite value stays one.  In a graph 64 ragged sequences on 4 key heads of
+        // 128 take 167 us, with one operand too; 8 of 16,384 slots on 4 key heads of 64, 16 query
+        // heads each, 32.7 us, 30.9 with one.
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const __nv_bfloat162 big = __floats2bfloat162_rn(p[2 * e], p[2 * e + 1]);
-          const __nv_bfloat162 rest =
-              __floats2bfloat162_rn(p[2 * e] - __low2float(big), p[2 * e + 1] - __high2float(big));
-          hi[i][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&big));
+          const uint32_t x0 = __float_as_uint(p[2 * e]), x1 = __float_as_uint(p[2 * e + 1]);
+          const __nv_bfloat162 rest = __floats2bfloat162_rn(remainder_of(p[2 * e]), remainder_of(p[2 * e + 1]));
+          hi[i][e] = transpose8x8(__byte_perm(x0, x1, 0x7632));
           lo[i][e] = transpose8x8(*reinterpret_cast<const uint32_t*>(&rest));
         }
       }

@@ -39,3 +39,24 @@ def test_decode_rounds_only_what_it_stores(d, H, G, lens):
         tol = np.einsum("hn,hnd->hd", p, np.abs(vr)) * rel[:, None] + 2.0 ** -8 * np.abs(want) * (1 + 2.0 ** -7)
         off = np.abs(np64(o[b, :, 0]) - want)
         assert np.all(off <= tol), (b, (off / tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,G", [(64, 1), (128, 3), (64, 16)])
+def test_decode_carries_an_infinite_value(dtype, d, G):
+    """An infinity among the values attended to is the output of its channel, with its sign
+    (a positive probability times it), infinities of both signs a NaN; other channels are as without it."""
+    from long_context_hierarchical_b200 import lh
+    c = Case([200, 5], 2, d, 16, dtype, seed=G)
+    q = normal(c.g, (2, 2 * G, 1, d), dtype)
+    want = lh.decode(c.cache, c.table, c.lengths, q)
+    for b, j, h, ch, x in ((0, 3, 0, 1, math.inf), (0, 150, 0, 2, -math.inf), (0, 199, 0, 2, -math.inf),
+                           (0, 60, 0, 40, math.inf), (0, 61, 0, 40, -math.inf), (1, 0, 1, 5, -math.inf)):
+        c.v[int(c.table[b, j // 16]), h, j % 16, ch] = x
+    o, lse = lh.decode(c.cache, c.table, c.lengths, q)
+    assert torch.equal(lse, want[1])
+    assert bool((o[0, :G, 0, 1] == math.inf).all()) and bool((o[0, :G, 0, 2] == -math.inf).all())
+    assert torch.isnan(o[0, :G, 0, 40]).all() and bool((o[1, G:, 0, 5] == -math.inf).all())
+    for b, heads, channels in ((0, slice(0, G), [1, 2, 40]), (1, slice(G, 2 * G), [5])):
+        o[b, heads, 0, channels] = want[0][b, heads, 0, channels]
+    assert torch.equal(o, want[0])
