@@ -375,7 +375,9 @@ lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, i
  * the entries behind are not touched.  A NaN among q, k and v makes the outputs that
  * it enters NaN; what lies behind a length is never read.  ws: lh_decode_ws_bytes() bytes, contents
  * on entry ignored; calls that overlap on the GPU (two streams, two graphs)
- * need one each.  Results do not depend on scheduling. */
+ * need one each.  Results do not depend on scheduling.  The size query returns
+ * -1 for a configuration that the call would refuse (lh_last_status() says with
+ * which status). */
 int64_t lh_decode_ws_bytes(const lh_cache* cache, int64_t Hq, int32_t with_weights);
 lh_status lh_decode(const lh_cache* cache, const lh_rows* Q, float scale, void* O, float* lse,
                     const float* weights, float* weights_out, void* ws, size_t ws_bytes,
@@ -415,6 +417,8 @@ lh_status lh_selftest_wait_timeout(lh_stream_t stream);
 
 const char* lh_status_string(lh_status s);
 const char* lh_last_error(void);
+/* The status that goes with lh_last_error(): why a size query returned -1. */
+lh_status lh_last_status(void);
 
 /* sizeof(lh_plan) as compiled into the library, for bindings to check their
  * mirror of the struct. */

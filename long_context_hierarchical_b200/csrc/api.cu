@@ -21,12 +21,15 @@ unsigned int* device_status_ptr() {
 }
 
 static thread_local std::string t_last_error;
+static thread_local lh_status t_last_status = LH_OK;
 
 lh_status fail(lh_status s, const std::string& why) {
+  t_last_status = s;
   t_last_error = why;
   return s;
 }
 lh_status ok() {
+  t_last_status = LH_OK;
   t_last_error.clear();
   return LH_OK;
 }
@@ -95,6 +98,7 @@ const char* lh_status_string(lh_status s) {
 }
 
 const char* lh_last_error(void) { return t_last_error.c_str(); }
+lh_status lh_last_status(void) { return t_last_status; }
 
 int64_t lh_plan_bytes(void) { return (int64_t)sizeof(lh_plan); }
 

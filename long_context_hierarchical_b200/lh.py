@@ -33,7 +33,7 @@ EXPORTS = (
     "lh_last_error", "lh_plan_bytes", "lh_attn_bwd_static", "lh_set_deterministic",
     "lh_selftest_wait_timeout", "lh_rotary_init", "lh_rotary_plan_bytes", "lh_rotary",
     "lh_cache_bytes", "lh_cache_append", "lh_decode_ws_bytes", "lh_decode", "lh_evict_ws_bytes",
-    "lh_evict",
+    "lh_evict", "lh_last_status",
 )
 
 
@@ -136,6 +136,8 @@ def _load():
     lib.lh_status_string.restype = ctypes.c_char_p
     lib.lh_last_error.argtypes = []
     lib.lh_last_error.restype = ctypes.c_char_p
+    lib.lh_last_status.argtypes = []
+    lib.lh_last_status.restype = ctypes.c_int
     lib.lh_plan_bytes.argtypes = []
     lib.lh_plan_bytes.restype = I64
     lib.lh_set_deterministic.argtypes = [ctypes.c_int]
@@ -652,7 +654,7 @@ class PagedCache:
             n = function(raw, *sizes)
             if n < 0:
                 if B:
-                    _check(LH_ERR_INVALID_ARG, where)
+                    _check(LIB.lh_last_status(), where)
                 return 0
             if len(self._needs) > 256:
                 self._needs.clear()

@@ -331,3 +331,34 @@ def test_workspace_sizes_follow_the_shapes():
     plain, more = (lh.decode_ws_bytes(kc, table, lens, 4, w) for w in (False, True))
     assert more == plain + 2 * 4 * 64 * 4
     assert lh.evict_ws_bytes(kc, table, lens, 64) < lh.evict_ws_bytes(kc, table, lens, 32)
+
+
+def test_size_queries_refuse_with_the_status_of_their_calls():
+    """What a call refuses as not built is not reported as an invalid argument by the scratch
+    size that the binding asks for before it, and the other way round."""
+    i32, bf = torch.int32, torch.bfloat16
+    table, lens = torch.zeros(2, 4, dtype=i32), torch.zeros(2, dtype=i32)
+
+    def kc(H=2, page=16, d=64):
+        return lh.PagedCache.of(*(torch.zeros(8, H, page, d, dtype=bf) for _ in range(2)))
+
+    for cache_, status in ((kc(page=48), lh.LH_ERR_UNSUPPORTED), (kc(d=32), lh.LH_ERR_UNSUPPORTED),
+                           (kc(H=0), lh.LH_ERR_INVALID_ARG)):
+        H, page, d = cache_.H, cache_.page, cache_.d
+        w = torch.zeros(2, H, 4 * page)
+        for call in (lambda: lh.decode(cache_, table, lens, torch.zeros(2, 2, 1, d, dtype=bf)),
+                     lambda: lh.decode_ws_bytes(cache_, table, lens, 2),
+                     lambda: lh.evict(cache_, table, lens, w, 8), lambda: lh.evict_ws_bytes(cache_, table, lens, 8)):
+            with pytest.raises(lh.LighthouseError) as e:
+                call()
+            assert e.value.status == status, str(e.value)
+    for call, status in ((lambda: lh.decode_ws_bytes(kc(), table, lens, 3), lh.LH_ERR_INVALID_ARG),
+                         (lambda: lh.decode_ws_bytes(kc(), table, lens, 1 << 22), lh.LH_ERR_UNSUPPORTED),
+                         (lambda: lh.evict_ws_bytes(kc(), table, lens, 0), lh.LH_ERR_INVALID_ARG)):
+        with pytest.raises(lh.LighthouseError) as e:
+            call()
+        assert e.value.status == status, str(e.value)
+    assert lh.LIB.lh_decode_ws_bytes(ctypes.byref(cache(page=17)), 4, 0) == -1
+    assert lh.LIB.lh_last_status() == lh.LH_ERR_UNSUPPORTED
+    assert lh.LIB.lh_evict_ws_bytes(ctypes.byref(cache()), 0) == -1
+    assert lh.LIB.lh_last_status() == lh.LH_ERR_INVALID_ARG
