@@ -895,10 +895,10 @@ def forward(pl: Plan, Q, K, V, O=None, ctx: Context | None = None, ws: Workspace
     must not change in between."""
     _require_tokens(pl, Q=Q, K=K, V=V)
     dev = Q.device
-    if rotary is not None:
-        Q, K = _rotate(rotary, _bhnd(pl, Q, K), None, positions, start, 0, stream)
     if O is None:
         O = torch.empty_like(Q)
+    if rotary is not None:
+        Q, K = _rotate(rotary, _bhnd(pl, Q, K), None, positions, start, 0, stream)
     if ctx is None:
         ctx = Context(pl, dev)
     if ws is None:

@@ -9,7 +9,7 @@ import torch
 
 from oracle import cache as oracle
 from tests.helpers import np64
-from tests.test_gpu_cache import U, Case, normal
+from tests.test_gpu_cache import U, Case, gen, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,19 @@ def test_decode_carries_an_infinite_value(dtype, d, G):
     for b, heads, channels in ((0, slice(0, G), [1, 2, 40]), (1, slice(G, 2 * G), [5])):
         o[b, heads, 0, channels] = want[0][b, heads, 0, channels]
     assert torch.equal(o, want[0])
+
+
+def test_layer_with_rotary_keeps_the_shape_of_its_queries():
+    """O has the shape of Q, with rotary as without it."""
+    from long_context_hierarchical_b200 import lh
+    g = gen(7)
+    B, H, N, d = 2, 3, 128, 64
+    pl = lh.plan(B, H, N, d, 4, 3, 4, "bf16")
+    rp = lh.rotary_plan(d)
+    Q, K, V = (normal(g, (B, H, N, d), "bf16") for _ in range(3))
+    want = lh.forward(pl, Q, K, V, rotary=rp)[0]
+    for shape in ((B * H, N, d), (B * H * N, d), (-1,)):
+        for k in (K, K.view(B * H, N, d)):
+            assert lh.forward(pl, Q.view(shape), k, V)[0].shape == Q.view(shape).shape
+            O = lh.forward(pl, Q.view(shape), k, V, rotary=rp)[0]
+            assert O.shape == Q.view(shape).shape and torch.equal(O.view(B, H, N, d), want)
