@@ -893,6 +893,8 @@ def forward(pl: Plan, Q, K, V, O=None, ctx: Context | None = None, ws: Workspace
     runs on Q and K turned to their positions (copies, as ``lh.rotary`` makes
     them), and the matching ``backward`` turns their gradients back; positions
     must not change in between."""
+    if rotary is None and (positions is not None or start != 0):
+        raise ValueError("positions, start: given without rotary")
     _require_tokens(pl, Q=Q, K=K, V=V)
     dev = Q.device
     if O is None:

@@ -362,3 +362,16 @@ def test_size_queries_refuse_with_the_status_of_their_calls():
     assert lh.LIB.lh_last_status() == lh.LH_ERR_UNSUPPORTED
     assert lh.LIB.lh_evict_ws_bytes(ctypes.byref(cache()), 0) == -1
     assert lh.LIB.lh_last_status() == lh.LH_ERR_INVALID_ARG
+
+
+def test_positions_without_rotary_are_refused():
+    """The layer would leave them unused, and its caller expects rows to be turned."""
+    pl = lh.plan(1, 2, 64, 64, 4, 2, 2, "bf16")
+    x = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16)
+    for kw in (dict(positions=torch.zeros(64, dtype=torch.int32)), dict(start=5)):
+        with pytest.raises(ValueError) as e:
+            lh.forward(pl, x, x, x, **kw)
+        assert "rotary" in str(e.value)
+    with pytest.raises(ValueError) as e:
+        lh.forward(pl, x, x, x)
+    assert "CUDA" in str(e.value)
