@@ -2,6 +2,7 @@
 repeated ones than the operators' own tests take.  Oracle and bounds are those of
 tests/test_gpu_cache.py."""
 import math
+import os
 
 import numpy as np
 import pytest
@@ -76,3 +77,57 @@ def test_layer_with_rotary_keeps_the_shape_of_its_queries():
             assert lh.forward(pl, Q.view(shape), k, V)[0].shape == Q.view(shape).shape
             O = lh.forward(pl, Q.view(shape), k, V, rotary=rp)[0]
             assert O.shape == Q.view(shape).shape and torch.equal(O.view(B, H, N, d), want)
+
+
+def test_readme_answering_example_over_many_steps():
+    """The README's steps (append, decode, evict), repeated as they stand with small sizes: what
+    is left in the cache are rows of the sequence turned at their own positions, the
+    newest among them, and the answer is dense attention over exactly these rows."""
+    from long_context_hierarchical_b200 import lh
+    text = open(os.path.join(os.path.dirname(os.path.dirname(__file__)), "README.md")).read()
+    block = next(x for x in text.split("```python\n")[1:] if "lh.cache_append" in x).split("```")[0]
+    B, H, d, page, width, budget, recent = 2, 2, 64, 16, 4, 40, 8
+    for a, b in (("49152", str(budget)), ("1024", str(recent)), ("4096", str(B * width)), ("page=64", f"page={page}"),
+                 ("H=16", f"H={H}")):
+        assert a in block
+        block = block.replace(a, b)
+    first, steps = block.split("\n", 1)
+    assert "PagedCache" in first
+    g = gen(14)
+    cap = width * page
+    i32 = dict(dtype=torch.int32, device="cuda")
+    env = dict(lh=lh, torch=torch, rp=lh.rotary_plan(d, base=500000.0), B=B,
+               table=torch.randperm(B * width, generator=g, **i32).view(B, width), lengths=torch.zeros(B, **i32),
+               seen=torch.zeros(B, **i32), weights=torch.zeros((B, H, cap), device="cuda"),
+               slot_positions=torch.full((B, H, cap), -1, **i32))
+    exec(first, env)
+    cache, total = env["cache"], 0
+    keys = torch.empty((B, H, 0, d), dtype=torch.bfloat16, device="cuda")   # of all rows so far, turned
+    values = keys.clone()
+    for T in [30, 1, 25, 1, 1, 20] + [1] * 20:
+        env["T"] = T
+        env["K"], env["V"], env["Q"] = (normal(g, (B, H, T, d), "bf16") for _ in range(3))
+        q = lh.rotary(env["rp"], env["Q"], start=total)[:, :, -1:]
+        keys = torch.cat((keys, lh.rotary(env["rp"], env["K"], start=total)), 2)
+        values = torch.cat((values, env["V"]), 2)
+        total += T
+        exec(steps, env)
+        for b in range(B):
+            n = int(env["lengths"][b])
+            assert n == min(total, budget)
+            at = torch.arange(n, device="cuda")
+            ids = env["table"][b].long()[at // page]
+            for h in range(H):
+                k, v = cache.k[ids, h, at % page], cache.v[ids, h, at % page]
+                same = (v[:, None] == values[b, h][None]).all(-1)       # which row stands in which slot
+                assert bool((same.sum(1) == 1).all())
+                row = same.int().argmax(1)
+                assert torch.equal(k, keys[b, h, row])                 # turned at its own position
+                kept = set(row.tolist())
+                assert len(kept) == n and set(range(total - min(recent, n), total)) <= kept
+        if total == T:   # the first step: every row was there
+            for b in range(B):
+                wo, _, p = oracle.decode(np64(q[b, :, 0]), np64(keys[b]), np64(values[b]), d ** -0.5)
+                T_o = np.einsum("hn,hnd->hd", p, np.abs(np64(values[b])))
+                assert np.all(np.abs(np64(env["O"][b, :, 0]) - wo) <= 2.0 ** -6 * (T_o + np.abs(wo)))
+    lh.device_status()
