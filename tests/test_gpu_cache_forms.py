@@ -10,7 +10,7 @@ import torch
 
 from oracle import cache as oracle
 from tests.helpers import np64
-from tests.test_gpu_cache import U, Case, gen, normal
+from tests.test_gpu_cache import U, Case, gen, make_weights, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -130,4 +130,50 @@ def test_readme_answering_example_over_many_steps():
                 wo, _, p = oracle.decode(np64(q[b, :, 0]), np64(keys[b]), np64(values[b]), d ** -0.5)
                 T_o = np.einsum("hn,hnd->hd", p, np.abs(np64(values[b])))
                 assert np.all(np.abs(np64(env["O"][b, :, 0]) - wo) <= 2.0 ** -6 * (T_o + np.abs(wo)))
+    lh.device_status()
+
+
+def check_evicted_heads(c, heads, budget, w0, p0, protect, got, k0, v0):
+    """Some heads of a single sequence: weights, positions and rows."""
+    table = c.table[0].long()
+    for h in heads:
+        _, moves, _ = oracle.evict(w0[0, h].cpu().numpy(), c.lens[0], budget,
+                                   None if p0 is None else p0[0, h].cpu().numpy(), protect)
+        src, dst = (torch.tensor(x, device="cuda") for x in zip(*moves))
+        want = torch.zeros(c.capacity, device="cuda")
+        want[:budget] = w0[0, h, :budget]
+        want[dst] = w0[0, h, src]
+        assert torch.equal(got[1][0, h], want)
+        if p0 is not None:
+            p = torch.full((c.capacity,), -1, dtype=torch.int32, device="cuda")
+            p[:budget] = p0[0, h, :budget]
+            p[dst] = p0[0, h, src]
+            assert torch.equal(got[2][0, h], p)
+        for x, x0 in ((c.k, k0), (c.v, v0)):
+            rows = x0[:, h].clone()
+            rows[table[dst // c.page], dst % c.page] = x0[table[src // c.page], h, src % c.page]
+            assert torch.equal(x[:, h].nan_to_num(9.0), rows.nan_to_num(9.0))
+
+
+@pytest.mark.parametrize("H,n,budget,protected,placed,in_place", [
+    *[(1, 330003, 100000, a, b, c) for a in (False, True) for b in (False, True) for c in (False, True)],
+    *[(H, n, n // 2, a, a, c) for H, n in ((80, 41003), (50, 82003)) for a in (False, True) for c in (False, True)]])
+def test_evict_reads_weights_again_where_keys_do_not_fit(H, n, budget, protected, placed, in_place):
+    """A block keeps the keys of at most 40960 slots in shared memory and at most eight
+    blocks share a head, so 330,003 slots never fit, however many blocks a head gets; where 148 SMs
+    are one block a head (two), 41,003 (82,003) slots do not either."""
+    from long_context_hierarchical_b200 import lh
+    assert n > 40960 * min(8, 148 // H)
+    c = Case([n], H, 64, 256, "bf16", seed=6)
+    w = make_weights(c, "ties" if protected else "spread")
+    w[:, :, n:] = 0.0
+    pos = torch.rand(w.shape, generator=c.g, device="cuda").argsort(-1).int() if placed else None
+    first = n - n // 4
+    protect = torch.tensor([first], dtype=torch.int32, device="cuda") if protected else None
+    k0, v0 = c.k.clone(), c.v.clone()
+    w0, p0 = w.clone(), None if pos is None else pos.clone()
+    got = lh.evict(c.cache, c.table, c.lengths, w, budget, positions=pos, protect=protect,
+                   weights_out=w if in_place else None, positions_out=pos if in_place else None)
+    assert int(got[0][0]) == budget
+    check_evicted_heads(c, (0,) if H == 1 else (0, H - 1), budget, w0, p0, first if protected else None, got, k0, v0)
     lh.device_status()
