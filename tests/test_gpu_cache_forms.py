@@ -177,3 +177,49 @@ def test_evict_reads_weights_again_where_keys_do_not_fit(H, n, budget, protected
     assert int(got[0][0]) == budget
     check_evicted_heads(c, (0,) if H == 1 else (0, H - 1), budget, w0, p0, first if protected else None, got, k0, v0)
     lh.device_status()
+
+
+@pytest.mark.parametrize("dtype,d,Hq,H,T", [("bf16", 64, 9, 3, 20001), ("bf16", 64, 6, 3, 40001),
+                                            ("bf16", 128, 2, 1, 20001), ("bf16", 128, 9, 3, 10001),
+                                            ("f32", 64, 2, 1, 40001), ("f32", 128, 4, 2, 20001)])
+def test_append_blocks_of_several_heads(dtype, d, Hq, H, T):
+    """Rows enough that a block takes several heads (all of them, or a part that begins
+    and ends inside Q, K or V): a pair of heads in flight is the last of Q and the first of K, or
+    the last of K and the first of V, and the last is alone.  The bits are those of lh.rotary and of
+    copies; padding is not read and nothing else is written."""
+    from long_context_hierarchical_b200 import lh
+    counts = [T, T // 2 + 3, T - 1]
+    lens = [counts[0] + 5, counts[1], counts[2] + 100]
+    c = Case(lens, H, d, 64, dtype, seed=Hq, width=-(-max(lens) // 64) + 1)
+    k0, v0 = c.k.nan_to_num(9.0), c.v.nan_to_num(9.0)
+    q = normal(c.g, (3, T, Hq, d), dtype).transpose(1, 2)
+    k, v = (normal(c.g, (3, H, T, d), dtype) for _ in range(2))
+    for b, m in enumerate(counts):   # padding that would show
+        for x in (q, k, v):
+            x[b, :, m:] = float("nan")
+    cnt = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    given = torch.randint(0, 500000, (3, T), generator=c.g, device="cuda", dtype=torch.int32)
+    slots = ((c.lengths - cnt)[:, None] + torch.arange(T, device="cuda", dtype=torch.int32)).int()
+    for rp, positions in ((lh.rotary_plan(d, rot=d // 2), None), (lh.rotary_plan(d, layout="interleaved"), given),
+                          (None, None)):
+        c.k.copy_(k0)
+        c.v.copy_(v0)
+        sp = torch.full((3, H, c.capacity), -9, dtype=torch.int32, device="cuda")
+        pos = slots if positions is None else positions
+        want_q, want_k = (q, k) if rp is None else lh.rotary(rp, q, k, positions=pos)
+        qi = q.clone()
+        out = lh.cache_append(c.cache, c.table, c.lengths, k, v, Q=qi, rotary=rp, positions=positions, counts=cnt,
+                              slot_positions=sp, out=qi)
+        assert out is qi
+        again = lh.cache_append(c.cache, c.table, c.lengths, k, v, Q=q, rotary=rp, positions=positions, counts=cnt)
+        assert torch.equal(again, qi)
+        k1, v1, sp1 = k0.clone(), v0.clone(), torch.full_like(sp, -9)
+        for b, m in enumerate(counts):
+            assert torch.equal(qi[b, :, :m], want_q[b, :, :m]) and not qi[b, :, m:].any()
+            at = slots[b, :m].long()
+            page, row = c.table[b].long()[at // 64], at % 64
+            k1[page, :, row] = want_k[b, :, :m].transpose(0, 1)
+            v1[page, :, row] = v[b, :, :m].transpose(0, 1)
+            sp1[b, :, at] = pos[b, :m]
+        assert torch.equal(c.k, k1) and torch.equal(c.v, v1) and torch.equal(sp, sp1)
+    lh.device_status()
