@@ -10,7 +10,7 @@ import torch
 
 from oracle import cache as oracle
 from tests.helpers import np64
-from tests.test_gpu_cache import U, Case, gen, make_weights, normal
+from tests.test_gpu_cache import U, Case, check_decode, gen, make_weights, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -223,3 +223,20 @@ def test_append_blocks_of_several_heads(dtype, d, Hq, H, T):
             sp1[b, :, at] = pos[b, :m]
         assert torch.equal(c.k, k1) and torch.equal(c.v, v1) and torch.equal(sp, sp1)
     lh.device_status()
+
+
+@pytest.mark.parametrize("dtype,d,Hq", [("bf16", 64, 3), ("f32", 64, 1), ("bf16", 128, 2), ("f32", 128, 1)])
+@pytest.mark.parametrize("n", [4096, 4097, 8192, 8193, 300001])
+def test_decode_join_of_many_parts(dtype, d, Hq, n):
+    """One key head, no weights: as many parts as tiles of 64 slots (64, 65, 128, 129) or
+    blocks (hundreds) are joined by the launch for few heads.  Its bits are those of the
+    launch that joins beside the weights."""
+    from long_context_hierarchical_b200 import lh
+    c = Case([n], 1, d, 1024, dtype, seed=n % 97)
+    q = normal(c.g, (1, Hq, 1, d), dtype)
+    o, lse = lh.decode(c.cache, c.table, c.lengths, q)
+    check_decode(c, q, o, lse)
+    w = torch.zeros((1, 1, c.capacity), device="cuda")
+    o2, lse2 = lh.decode(c.cache, c.table, c.lengths, q, weights=w)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check_decode(c, q, o, lse, weights=torch.zeros_like(w), weights_out=w)
