@@ -814,7 +814,18 @@ join_kernel(const __grid_constant__ DecodeCall k) {
 }
 
 // Calls f.template operator()<Core>() for the core that serves gv query heads a
-// key head.
+// key head.  Measured in a graph (us; 16,384 slots unless said otherwise):
+//   bf16, 64 sequences on 4 key heads of 64: 8 heads 169 in one group of eight, 184 in two;
+//     16 heads 192 in two groups, 331 as two parts of one group;
+//   fp32, as heads of a warp x warps of a tile, channels 64 | 128:
+//     1 (1 sequence of 98,304 slots, 1024 channels in all)   1x1 119 | 119, 2x1 128 | 123;
+//     2 (4 sequences, 512 channels)      2x1 51 | 48, 1x2 60 | 56, 2x2 74 | 67;
+//     3, 4 (32 sequences, 512 channels)  2x2 514 | 467, two parts in 2x1 646 | 636; 4x1 504,
+//       but 2 sequences of 3000 slots on 2 key heads 8.8 in place of 8.1;
+//     8 (the same)                       2x4 992 | 878, two parts of four 998 | 918;
+//     16 (the same)                      4x4 1924, four parts of four 1984 | 1825, two of eight | 1744.
+//   A core's time does not fall with the heads it lacks: 12 heads take 1921 | 1743, where three
+//   parts of four would take 1490 | 1373.
 template <typename F>
 void with_core(int dtype, int d, int gv, F&& f) {
   if (dtype == LH_BF16) {
@@ -848,7 +859,9 @@ Sizes sizes(const lh_cache& c, int64_t Hq, bool with_weights) {
   Sizes s{};
   const int64_t G = Hq / c.H;
   // Query heads that one block serves at most: 16, or 8 where an fp32 row of 128
-  // channels leaves registers for no more.
+  // channels leaves registers for no more.  More are cut into parts that each go through the
+  // cache: 64 sequences of 16,384 slots on 4 key heads of 64 channels, bf16, take 192 us in a
+  // graph with 16 heads a key head, 370 with 32 and 571 with 40.
   const int most_heads = c.dtype == LH_F32 && c.d == 128 ? 8 : 16;
   s.nv = (int)((G + most_heads - 1) / most_heads);
   s.gv = (int)((G + s.nv - 1) / s.nv);
