@@ -317,7 +317,8 @@ typedef struct {
  * positions[b * positions_stride + n], or at start + n where positions is
  * NULL (within 32 bits, like them).  transpose != 0 applies the transposed map, which is the gradient of
  * the plain one.  Y[i] may be X[i] itself (same pointer and strides);
- * otherwise none of the Y may overlap another tensor of the call.  Inputs may
+ * otherwise none of the Y may overlap another tensor of the call, and Y[i] lies
+ * before or behind all of X[i] (rows that interleave are refused).  Inputs may
  * repeat rows by zero strides, outputs may not.  fp32 arithmetic, rounded
  * once. */
 lh_status lh_rotary(const lh_rotary_plan* plan, int32_t dtype, int64_t B, int64_t N, int32_t count,

@@ -581,7 +581,8 @@ def _pair(Q, K, out):
 def rotary(rp: RotaryPlan, Q, K=None, positions=None, start: int = 0, out=None, stream=None):
     """Q, or (Q, K), [B, H, N, d] with any strides between rows, turned to their
     positions: positions[b, n] (int32, [N] or [B, N]) or start + n.  Returns new
-    contiguous tensors, or writes ``out`` (which may be the inputs themselves)."""
+    contiguous tensors, or writes ``out``, which may be the inputs themselves and lies
+    otherwise apart from them (rows that interleave with its input's are refused)."""
     X, Y = _pair(Q, K, out)
     got = _rotate(rp, X, Y, positions, start, 0, stream)
     return got[0] if K is None else got
@@ -797,7 +798,8 @@ def evict(cache: PagedCache, table, lengths, weights, budget: int, positions=Non
     earlier evictions have moved them.  Kept rows at low slots stay, the others
     fill the slots given up, so the order of slots is not that of positions;
     behind the new length weights are 0 and positions -1.  weights_out and
-    positions_out (default: new tensors) may be the inputs themselves.  ws: a
+    positions_out (default: new tensors) may be the inputs themselves.  No two
+    sequences may share a page, for both would move its rows.  ws: a
     uint8 scratch tensor of evict_ws_bytes(); calls that overlap on the GPU
     need one each (default: a new one)."""
     raw, B, capacity = cache._raw(table, lengths)
