@@ -374,7 +374,9 @@ lh_status lh_cache_append(const lh_cache* cache, const lh_rotary_plan* rotary, i
  * neither, possibly the same array): for every slot j < lengths[b]
  *   weights_out[b,h,j] = weights[b,h,j] + sum over head h's queries exp(s_j - lse);
  * the entries behind are not touched.  A NaN among q, k and v makes the outputs that
- * it enters NaN; what lies behind a length is never read.  ws: lh_decode_ws_bytes() bytes, contents
+ * it enters NaN; what lies behind a length is never read.  Sums are divided by
+ * their weight at the end, so values near the largest of fp32 (above 2^119 / lengths[b])
+ * may overflow.  ws: lh_decode_ws_bytes() bytes, contents
  * on entry ignored; calls that overlap on the GPU (two streams, two graphs)
  * need one each.  Results do not depend on scheduling.  The size query returns
  * -1 for a configuration that the call would refuse (lh_last_status() says with
